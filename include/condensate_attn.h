@@ -330,6 +330,111 @@ CA_API ca_status condensate_attn_status(void* workspace, void* stream);
  */
 CA_API ca_status condensate_attn_test_stall(unsigned long long limit_ns);
 
+/*
+ * ---------------------------------------------------------------------
+ * Operators around the attention.
+ *
+ * A [B, n, heads] grid of rows of d contiguous elements: row (b, t, h) starts
+ * at data + b stride_b + t stride_t + h stride_h (strides in elements, each
+ * a non-negative multiple of 16 bytes; data 16-byte aligned).  The parts of
+ * a fused projection [B, n, (Hq + 2 Hkv) d] and the rows of a [B, H, n, d]
+ * tensor, or of a slice of a longer cache [B, H, L, d], are all such grids.
+ */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_t, stride_h;
+} ca_rows;
+
+/*
+ * Parameters of condensate_attn_norm_rope.
+ *
+ *   q_weight, k_weight  [d] norm weights in w_dtype; NULL leaves that
+ *         tensor without a norm.  With one, a row becomes
+ *         x rsqrt(mean(x^2) + eps) w.
+ *   inv_freq  [rot_dim / 2] fp32.  After the norm, pair c of a row's leading
+ *         rot_dim elements turns by the angle position * inv_freq[c]:
+ *         (a, b) -> (a cos - b sin, b cos + a sin).  Pairs are (c, c +
+ *         rot_dim / 2), or (2c, 2c + 1) with interleaved != 0.  rot_dim is a
+ *         multiple of 16 in [0, d]; 0 rotates nothing.  The angle is formed
+ *         in 64 bits, so far positions lose nothing.
+ *   positions  [B, n] int32, or NULL: position pos0 + t for token t.
+ * Arithmetic is fp32, each result rounded once.
+ */
+typedef struct {
+  const void* q_weight;
+  const void* k_weight;
+  ca_dtype w_dtype;
+  float eps;
+  const float* inv_freq;
+  int rot_dim;
+  int interleaved;
+  const int32_t* positions;
+  int pos0;
+} ca_norm_rope;
+
+/*
+ * Per-head norm of queries and keys, position rotation and move into the
+ * layout of the attention entry points, one launch.  in[0..2] are the rows
+ * of q (Hq heads), k and v (Hkv heads) as a projection wrote them, out[0..2]
+ * where the results go; v is moved only.  k or v may be left out (data NULL
+ * in both).  Written grids must not overlap each other or an input, except
+ * that out[i] may be in[i] itself (same address and strides).  dtype covers
+ * inputs and outputs; d in {64, 128}.  No workspace, any stream.
+ */
+CA_API ca_status condensate_attn_norm_rope(const ca_rows* in, ca_dtype dtype,
+                                           int B, int n, int Hq, int Hkv,
+                                           int d, const ca_norm_rope* p,
+                                           const ca_rows* out, void* stream);
+
+/*
+ * Backward of condensate_attn_norm_rope.  grad_out[0..2]: gradients of its
+ * results; in[0..1]: its q and k inputs (needed where there is a norm
+ * weight; in may be NULL without any); grad_in[0..2]: gradients of q, k, v
+ * (may be the parts of one fused buffer).  grad_q_weight, grad_k_weight [d]
+ * in w_dtype, each may be NULL (always without that weight); they are summed
+ * in fp32 in a fixed order.  workspace: at least
+ * condensate_attn_norm_rope_workspace_size(d) bytes, 16-byte aligned, needed
+ * when a weight gradient is asked for.
+ */
+CA_API size_t condensate_attn_norm_rope_workspace_size(int d);
+CA_API ca_status condensate_attn_norm_rope_backward(
+    const ca_rows* grad_out, const ca_rows* in, ca_dtype dtype, int B, int n,
+    int Hq, int Hkv, int d, const ca_norm_rope* p, const ca_rows* grad_in,
+    void* grad_q_weight, void* grad_k_weight, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of condensate_attn_prefill_ex: gradients of Q, K and V from dO
+ * [B, Hq, nq, d] (in o_dtype), with the selected positions held constant.
+ * Q, K, V, dtype, sizes, W, k, W_i, W_h are those of the forward call (k the
+ * scalar one when per-head k_h were given), idx, idx_count and C_max what it
+ * wrote.  The probabilities are recomputed; neither O nor a log-sum-exp is
+ * read.  dQ [B, Hq, nq, d] and dK, dV [B, Hkv, L, d] are written whole, in
+ * dtype (keys that no row attends to get zeros).  Sums are fp32 in an order
+ * fixed by the inputs: equal calls give equal bits.
+ *
+ * Of a row's idx entries only the Top-k ones are read (slots 1 .. |C_i| - 1
+ * - W_i).  One outside [1, i - W_i], or a count that does not fit the row's
+ * window, k and C_max (a row the forward reported as overflowing C_max, or
+ * the idx of another call), raises CA_ERR_DEVICE_ARG through
+ * condensate_attn_status(); nothing outside the buffers is touched, the
+ * gradients are then those of the entries that fit.
+ *
+ * The workspace (query its size; it grows with B Hq nq (k + 1)) must not be
+ * shared by calls that overlap.  CA_ERR_UNSUPPORTED where one kv head has
+ * 2^31 or more slots ((Hq / Hkv) nq (k + 1)).
+ */
+CA_API size_t condensate_attn_prefill_backward_workspace_size(
+    ca_dtype dtype, ca_dtype o_dtype, int B, int nq, int L, int Hq, int Hkv,
+    int d, int k);
+CA_API ca_status condensate_attn_prefill_backward(
+    const void* Q, const void* K, const void* V, ca_dtype dtype,
+    const void* dO, ca_dtype o_dtype, int B, int nq, int L, int Hq, int Hkv,
+    int d, int W, int k, const int32_t* W_i, const int32_t* W_h,
+    const int32_t* idx, const int32_t* idx_count, int C_max, void* dQ,
+    void* dK, void* dV, void* workspace, size_t workspace_bytes,
+    void* stream);
+
 /* Static, human-readable name of a status code. */
 CA_API const char* condensate_attn_status_string(ca_status s);
 

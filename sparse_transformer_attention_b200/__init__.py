@@ -14,4 +14,9 @@ from .binding import (  # noqa: F401
     condensate_attn_workspace_size, condensate_attn_workspace_size_ex, load,
     status_string,
 )
+from .block import (  # noqa: F401,E402
+    attention, condensate_attn_norm_rope, condensate_attn_norm_rope_backward,
+    condensate_attn_prefill_backward,
+    condensate_attn_prefill_backward_workspace_size, norm_rope, qkv_attention,
+)
 from .sharded import decode_sharded, shard_bounds  # noqa: F401,E402

@@ -42,10 +42,27 @@ class CaExtras(ctypes.Structure):
                 ("mass", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
 
 
+class CaRows(ctypes.Structure):
+    """ca_rows of the header: a [B, n, heads] grid of rows of d elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
+                ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
+
+
+class CaNormRope(ctypes.Structure):
+    """ca_norm_rope of the header."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("w_dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int),
+                ("positions", ctypes.c_void_p), ("pos0", ctypes.c_int)]
+
+
 # (name, restype, argtypes) of every entry point the header declares.
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _X = ctypes.POINTER(CaExtras)
+_R = ctypes.POINTER(CaRows)
+_N = ctypes.POINTER(CaNormRope)
 SIGNATURES = {
     "condensate_attn_workspace_size":
         (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
@@ -78,6 +95,17 @@ SIGNATURES = {
               _P, _P, _P, _I, _P, ctypes.c_size_t, _P]),
     "condensate_attn_decode_shard_combine":
         (_I, [_P, _I, _I, _I, _I, _P, _I, _P]),
+    "condensate_attn_norm_rope":
+        (_I, [_R, _I, _I, _I, _I, _I, _I, _N, _R, _P]),
+    "condensate_attn_norm_rope_workspace_size": (ctypes.c_size_t, [_I]),
+    "condensate_attn_norm_rope_backward":
+        (_I, [_R, _R, _I, _I, _I, _I, _I, _I, _N, _R, _P, _P, _P,
+              ctypes.c_size_t, _P]),
+    "condensate_attn_prefill_backward_workspace_size":
+        (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
+    "condensate_attn_prefill_backward":
+        (_I, [_P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P,
+              _P, _P, _I, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "condensate_attn_status": (_I, [_P, _P]),
     "condensate_attn_test_stall": (_I, [ctypes.c_ulonglong]),
     "condensate_attn_status_string": (ctypes.c_char_p, [_I]),

@@ -1,0 +1,439 @@
+"""The operators around the attention, and their autograd forms.
+
+condensate_attn_norm_rope takes the rows of a projection, token-major
+[B, n, heads, d], through the per-head norm of queries and keys and the
+position rotation into the [B, H, n, d] layout that condensate_attn_prefill
+and condensate_attn_decode read (or into the rows of a cache);
+condensate_attn_norm_rope_backward and condensate_attn_prefill_backward are
+the gradients.  norm_rope, attention and qkv_attention are the same
+operators under torch.autograd.
+
+As in `binding`, this module marshals arguments; the computation runs in the
+library's kernels.  Calls run on the device of their tensors, on `stream` (by
+default that device's current stream), and wait for nothing, so they can be
+captured into CUDA graphs.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import binding
+from .binding import CaNormRope, CaRows, _check, _dt, _ptr, _require
+
+_DTYPES = (torch.float32, torch.bfloat16)
+
+
+@contextlib.contextmanager
+def _on(dev: torch.device, stream):
+    """The raw stream to launch on, with `dev` current and what is allocated
+    inside belonging to that stream."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, tensors on {dev}")
+        with torch.cuda.stream(stream):
+            yield ctypes.c_void_p(stream.cuda_stream)
+    elif torch.cuda.current_device() == dev.index:
+        yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _expect(t: torch.Tensor, name: str, shape, dtype, dev):
+    """Shape, type and device of one argument."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, "
+                         f"got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _dense(t: torch.Tensor, name: str, shape, dtype, dev):
+    _expect(t, name, shape, dtype, dev)
+    _require(t, name)
+
+
+def _grid(t: Optional[torch.Tensor], head_major: bool, name: str):
+    """ca_rows of a [B, n, H, d] tensor ([B, H, n, d] when head_major)."""
+    if t is None:
+        return CaRows()
+    sb, s1, s2, sd = t.stride()
+    B, n1, n2, _ = t.shape
+    if sd != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    # the stride of a dimension of one element says nothing
+    sb, s1, s2 = sb if B > 1 else 0, s1 if n1 > 1 else 0, s2 if n2 > 1 else 0
+    return CaRows(t.data_ptr(), sb, s2, s1) if head_major else \
+        CaRows(t.data_ptr(), sb, s1, s2)
+
+
+def _rope_params(d, n_tokens, dev, inv_freq, q_weight, k_weight, eps,
+                 positions, pos0, interleaved) -> CaNormRope:
+    w_dtype = None
+    for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            if w.dtype not in _DTYPES or (w_dtype not in (None, w.dtype)):
+                raise TypeError("q_weight and k_weight must both be float32 "
+                                "or both bfloat16")
+            w_dtype = w.dtype
+            _dense(w, nm, (d,), None, dev)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _dense(inv_freq, "inv_freq", (rot // 2,), torch.float32, dev)
+    if positions is not None:
+        _dense(positions, "positions", n_tokens, torch.int32, dev)
+    return CaNormRope(
+        None if q_weight is None else q_weight.data_ptr(),
+        None if k_weight is None else k_weight.data_ptr(),
+        binding.CA_F32 if w_dtype is None else _dt(w_dtype), eps,
+        None if inv_freq is None else inv_freq.data_ptr(), rot,
+        int(interleaved),
+        None if positions is None else positions.data_ptr(), pos0)
+
+
+def _sizes(q, k, v):
+    """(B, n, Hq, Hkv, d) of token-major q, k, v, checked against each other."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, n, Hq, d]")
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    B, n, Hq, d = q.shape
+    Hkv = k.shape[2] if k is not None else v.shape[2] if v is not None else 1
+    for t, nm in ((k, "k"), (v, "v")):
+        if t is not None:
+            _expect(t, nm, (B, n, Hkv, d), q.dtype, q.device)
+    return B, n, Hq, Hkv, d
+
+
+def condensate_attn_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor],
+                              v: Optional[torch.Tensor],
+                              inv_freq: Optional[torch.Tensor],
+                              q_weight: Optional[torch.Tensor] = None,
+                              k_weight: Optional[torch.Tensor] = None,
+                              eps: float = 1e-6,
+                              positions: Optional[torch.Tensor] = None,
+                              pos0: int = 0, interleaved: bool = False,
+                              Q: Optional[torch.Tensor] = None,
+                              K: Optional[torch.Tensor] = None,
+                              V: Optional[torch.Tensor] = None, stream=None):
+    """Norm of each query and key head (rows with a weight), position
+    rotation, and the move into the attention's layout, in one launch.
+
+    q [B, n, Hq, d], k and v [B, n, Hkv, d] (fp32 or bf16, last dimension
+    contiguous, any other strides: the parts of a fused projection need no
+    copy; k and v may be None).  inv_freq [rot / 2] float32 (None: no
+    rotation); positions [B, n] int32, else token t is at pos0 + t.  Q
+    [B, Hq, n, d], K, V [B, Hkv, n, d] are written where given, e.g. rows of
+    a cache `Kc[:, :, p:p + n]`, else allocated.
+
+    Returns (Q, K, V).
+    """
+    B, n, Hq, Hkv, d = _sizes(q, k, v)
+    dev = q.device
+    par = _rope_params(d, (B, n), dev, inv_freq, q_weight, k_weight, eps,
+                       positions, pos0, interleaved)
+    with _on(dev, stream) as s:
+        outs = []
+        for x, y, H, nm in ((q, Q, Hq, "Q"), (k, K, Hkv, "K"),
+                            (v, V, Hkv, "V")):
+            if x is None:
+                if y is not None:
+                    raise ValueError(f"{nm} given without its input")
+            elif y is None:
+                y = torch.empty((B, H, n, d), dtype=x.dtype, device=dev)
+            else:
+                _expect(y, nm, (B, H, n, d), q.dtype, dev)
+            outs.append(y)
+        code = binding.load().condensate_attn_norm_rope(
+            (CaRows * 3)(_grid(q, False, "q"), _grid(k, False, "k"),
+                         _grid(v, False, "v")),
+            _dt(q.dtype), B, n, Hq, Hkv, d, ctypes.byref(par),
+            (CaRows * 3)(_grid(outs[0], True, "Q"), _grid(outs[1], True, "K"),
+                         _grid(outs[2], True, "V")), s)
+    _check(code, "condensate_attn_norm_rope")
+    return tuple(outs)
+
+
+def condensate_attn_norm_rope_backward(
+        dQ: torch.Tensor, dK: Optional[torch.Tensor],
+        dV: Optional[torch.Tensor], q: Optional[torch.Tensor],
+        k: Optional[torch.Tensor], inv_freq: Optional[torch.Tensor],
+        q_weight: Optional[torch.Tensor] = None,
+        k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+        positions: Optional[torch.Tensor] = None, pos0: int = 0,
+        interleaved: bool = False, dq: Optional[torch.Tensor] = None,
+        dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+        weight_grads: bool = True, workspace: Optional[torch.Tensor] = None,
+        stream=None):
+    """Gradients of condensate_attn_norm_rope from dQ [B, Hq, n, d], dK, dV
+    [B, Hkv, n, d] and its inputs q, k (needed only with a norm weight).  dq,
+    dk, dv (token-major; e.g. the parts of one fused gradient) are written
+    where given.  weight_grads=False leaves the weights' gradients out.
+
+    Returns (dq, dk, dv, dq_weight, dk_weight), None where there is none.
+    """
+    if dQ.dim() != 4 or not dQ.is_cuda:
+        raise ValueError("dQ must be a CUDA tensor [B, Hq, n, d]")
+    B, Hq, n, d = dQ.shape
+    Hkv = dK.shape[1] if dK is not None else \
+        dV.shape[1] if dV is not None else 1
+    dev, dt = dQ.device, dQ.dtype
+    for t, nm in ((dK, "dK"), (dV, "dV")):
+        if t is not None:
+            _expect(t, nm, (B, Hkv, n, d), dt, dev)
+    if dK is None:
+        k_weight = None
+    for t, w, H, nm in ((q, q_weight, Hq, "q"), (k, k_weight, Hkv, "k")):
+        if w is not None:
+            if t is None:
+                raise ValueError(f"{nm} is needed for the norm's gradient")
+            _expect(t, nm, (B, n, H, d), dt, dev)
+    q, k = q if q_weight is not None else None, \
+        k if k_weight is not None else None
+    par = _rope_params(d, (B, n), dev, inv_freq, q_weight, k_weight, eps,
+                       positions, pos0, interleaved)
+    with _on(dev, stream) as s:
+        outs = []
+        for g, x, H, nm in ((dQ, dq, Hq, "dq"), (dK, dk, Hkv, "dk"),
+                            (dV, dv, Hkv, "dv")):
+            if g is None:
+                if x is not None:
+                    raise ValueError(f"{nm} given without its gradient")
+            elif x is None:
+                x = torch.empty((B, n, H, d), dtype=dt, device=dev)
+            else:
+                _expect(x, nm, (B, n, H, d), dt, dev)
+            outs.append(x)
+        dqw = torch.empty_like(q_weight) \
+            if weight_grads and q_weight is not None else None
+        dkw = torch.empty_like(k_weight) \
+            if weight_grads and k_weight is not None else None
+        lib = binding.load()
+        if (dqw is not None or dkw is not None) and workspace is None:
+            workspace = torch.empty(
+                lib.condensate_attn_norm_rope_workspace_size(d),
+                dtype=torch.uint8, device=dev)
+        if workspace is not None:
+            _require(workspace, "workspace")
+        code = lib.condensate_attn_norm_rope_backward(
+            (CaRows * 3)(_grid(dQ, True, "dQ"), _grid(dK, True, "dK"),
+                         _grid(dV, True, "dV")),
+            (CaRows * 3)(_grid(q, False, "q"), _grid(k, False, "k")),
+            _dt(dt), B, n, Hq, Hkv, d, ctypes.byref(par),
+            (CaRows * 3)(_grid(outs[0], False, "dq"),
+                         _grid(outs[1], False, "dk"),
+                         _grid(outs[2], False, "dv")),
+            _ptr(dqw), _ptr(dkw), _ptr(workspace),
+            0 if workspace is None else workspace.numel() *
+            workspace.element_size(), s)
+    _check(code, "condensate_attn_norm_rope_backward")
+    return (*outs, dqw, dkw)
+
+
+def condensate_attn_prefill_backward_workspace_size(
+        dtype: torch.dtype, o_dtype: torch.dtype, B: int, nq: int, L: int,
+        Hq: int, Hkv: int, d: int, k: int) -> int:
+    return int(binding.load().condensate_attn_prefill_backward_workspace_size(
+        _dt(dtype), _dt(o_dtype), B, nq, L, Hq, Hkv, d, k))
+
+
+def condensate_attn_prefill_backward(
+        Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, dO: torch.Tensor,
+        idx: torch.Tensor, idx_count: torch.Tensor, W: int, k: int,
+        W_i: Optional[torch.Tensor] = None,
+        W_h: Optional[torch.Tensor] = None,
+        dQ: Optional[torch.Tensor] = None, dK: Optional[torch.Tensor] = None,
+        dV: Optional[torch.Tensor] = None,
+        workspace: Optional[torch.Tensor] = None, stream=None
+        ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of condensate_attn_prefill with respect to Q, K and V, the
+    sets held constant: Q [B, Hq, nq, d], K, V [B, Hkv, L, d], W, k, W_i and
+    W_h as in the forward call, idx [B, Hq, nq, C_max] and idx_count
+    [B, Hq, nq] as it returned them, dO [B, Hq, nq, d] of O's type.  With a
+    workspace of the caller's (the size function's bytes) the device status
+    can be read by condensate_attn_status.
+
+    Returns (dQ, dK, dV) in the type of Q; equal calls give equal bits.
+    """
+    if Q.dim() != 4 or K.dim() != 4:
+        raise ValueError("Q and K must be [B, H, n, d]")
+    B, Hq, nq, d = Q.shape
+    Hkv, L = K.shape[1], K.shape[2]
+    dev, dt = Q.device, Q.dtype
+    _require(Q, "Q")
+    _dense(K, "K", (B, Hkv, L, d), dt, dev)
+    _dense(V, "V", (B, Hkv, L, d), dt, dev)
+    _dense(dO, "dO", (B, Hq, nq, d), None, dev)
+    _dense(idx, "idx", (B, Hq, nq, idx.shape[-1]), torch.int32, dev)
+    _dense(idx_count, "idx_count", (B, Hq, nq), torch.int32, dev)
+    if W_i is not None:
+        _dense(W_i, "W_i", (B, nq), torch.int32, dev)
+    if W_h is not None:
+        _dense(W_h, "W_h", (Hq,), torch.int32, dev)
+    with _on(dev, stream) as s:
+        if dQ is None:
+            dQ = torch.empty_like(Q)
+        if dK is None:
+            dK = torch.empty_like(K)
+        if dV is None:
+            dV = torch.empty_like(V)
+        _dense(dQ, "dQ", Q.shape, dt, dev)
+        _dense(dK, "dK", K.shape, dt, dev)
+        _dense(dV, "dV", V.shape, dt, dev)
+        if workspace is None:
+            workspace = torch.empty(
+                condensate_attn_prefill_backward_workspace_size(
+                    dt, dO.dtype, B, nq, L, Hq, Hkv, d, k),
+                dtype=torch.uint8, device=dev)
+        _require(workspace, "workspace")
+        code = binding.load().condensate_attn_prefill_backward(
+            _ptr(Q), _ptr(K), _ptr(V), _dt(dt), _ptr(dO), _dt(dO.dtype), B,
+            nq, L, Hq, Hkv, d, int(W), int(k), _ptr(W_i), _ptr(W_h),
+            _ptr(idx), _ptr(idx_count), idx.shape[-1], _ptr(dQ), _ptr(dK),
+            _ptr(dV), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), s)
+    _check(code, "condensate_attn_prefill_backward")
+    return dQ, dK, dV
+
+
+# ---------------------------------------------------------------- autograd
+def _readable(t: torch.Tensor) -> torch.Tensor:
+    """t itself if the kernels can read its rows where they are (an incoming
+    gradient may be an expanded scalar, or start off a 16-byte boundary)."""
+    step = 16 // t.element_size()
+    ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(
+        n == 1 or s % step == 0 for n, s in zip(t.shape[:-1], t.stride()))
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
+
+
+def _save_rope(ctx, q, k, inv_freq, q_weight, k_weight, positions, scalars):
+    ctx.rope = scalars  # eps, pos0, interleaved
+    ctx.save_for_backward(q if q_weight is not None else None,
+                          k if k_weight is not None else None, inv_freq,
+                          q_weight, k_weight, positions)
+
+
+def _rope_backward(ctx, grads, need_q_weight, need_k_weight, **parts):
+    q, k, inv_freq, q_weight, k_weight, positions = ctx.saved_tensors
+    eps, pos0, interleaved = ctx.rope
+    dq, dk, dv, dqw, dkw = condensate_attn_norm_rope_backward(
+        *(_readable(g) for g in grads), q, k, inv_freq, q_weight, k_weight,
+        eps, positions, pos0, interleaved,
+        weight_grads=need_q_weight or need_k_weight, **parts)
+    return (dq, dk, dv, dqw if need_q_weight else None,
+            dkw if need_k_weight else None)
+
+
+class _NormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, inv_freq, q_weight, k_weight, eps, positions,
+                pos0, interleaved):
+        q, k, v = _readable(q), _readable(k), _readable(v)
+        _save_rope(ctx, q, k, inv_freq, q_weight, k_weight, positions,
+                   (eps, pos0, interleaved))
+        return condensate_attn_norm_rope(q, k, v, inv_freq, q_weight,
+                                         k_weight, eps, positions, pos0,
+                                         interleaved)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        need = ctx.needs_input_grad
+        dq, dk, dv, dqw, dkw = _rope_backward(ctx, grads, need[4], need[5])
+        return dq, dk, dv, None, dqw, dkw, None, None, None, None
+
+
+def _parts(x, Hq, Hkv):
+    """The q, k and v rows of a fused [B, n, Hq + 2 Hkv, d] tensor."""
+    return x[:, :, :Hq], x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:]
+
+
+class _FusedNormRope(torch.autograd.Function):
+    """_NormRope on a fused projection; its gradient is one buffer too."""
+
+    @staticmethod
+    def forward(ctx, x, Hq, Hkv, inv_freq, q_weight, k_weight, eps, positions,
+                pos0, interleaved):
+        x = _readable(x)
+        q, k, v = _parts(x, Hq, Hkv)
+        ctx.heads = (Hq, Hkv, x.shape)
+        _save_rope(ctx, q, k, inv_freq, q_weight, k_weight, positions,
+                   (eps, pos0, interleaved))
+        return condensate_attn_norm_rope(q, k, v, inv_freq, q_weight,
+                                         k_weight, eps, positions, pos0,
+                                         interleaved)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        Hq, Hkv, shape = ctx.heads
+        need = ctx.needs_input_grad
+        dx = torch.empty(shape, dtype=grads[0].dtype, device=grads[0].device)
+        dq, dk, dv = _parts(dx, Hq, Hkv)
+        _, _, _, dqw, dkw = _rope_backward(ctx, grads, need[4], need[5],
+                                           dq=dq, dk=dk, dv=dv)
+        return dx, None, None, None, dqw, dkw, None, None, None, None
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, Q, K, V, W, k, W_i, W_h, k_h, o_dtype):
+        Q, K, V = Q.contiguous(), K.contiguous(), V.contiguous()
+        with torch.cuda.device(Q.device):
+            O, idx, count = binding.condensate_attn_prefill(
+                Q, K, V, W, k, W_i=W_i, o_dtype=o_dtype, W_h=W_h, k_h=k_h)
+        ctx.sizes = (W, k)
+        ctx.save_for_backward(Q, K, V, idx, count, W_i, W_h)
+        ctx.mark_non_differentiable(idx, count)
+        return O, idx, count
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dO, _idx, _count):
+        Q, K, V, idx, count, W_i, W_h = ctx.saved_tensors
+        W, k = ctx.sizes
+        dQ, dK, dV = condensate_attn_prefill_backward(
+            Q, K, V, _readable(dO).contiguous(), idx, count, W, k, W_i=W_i,
+            W_h=W_h)
+        return dQ, dK, dV, None, None, None, None, None, None
+
+
+def norm_rope(q, k, v, inv_freq, q_weight=None, k_weight=None,
+              eps: float = 1e-6, positions=None, pos0: int = 0,
+              interleaved: bool = False):
+    """condensate_attn_norm_rope under autograd: gradients reach q, k, v and
+    the weights.  Returns (Q, K, V)."""
+    return _NormRope.apply(q, k, v, inv_freq, q_weight, k_weight, eps,
+                           positions, pos0, interleaved)
+
+
+def attention(Q, K, V, W: int, k: int, W_i=None, W_h=None, k_h=None,
+              o_dtype: torch.dtype = torch.float32):
+    """condensate_attn_prefill under autograd: gradients reach Q, K and V,
+    the selected positions being constants.  Returns (O, idx, idx_count)."""
+    return _Attention.apply(Q, K, V, W, k, W_i, W_h, k_h, o_dtype)
+
+
+def qkv_attention(qkv, Hq: int, Hkv: int, W: int, k: int, inv_freq,
+                  q_weight=None, k_weight=None, eps: float = 1e-6,
+                  positions=None, pos0: int = 0, interleaved: bool = False,
+                  W_i=None, W_h=None, k_h=None, o_dtype=None):
+    """The attention of a layer from its fused projection qkv
+    [B, n, (Hq + 2 Hkv) d]: norm and rotation, then the prefill, under
+    autograd.  Returns O [B, Hq, n, d] in o_dtype (qkv's type by default)."""
+    heads = Hq + 2 * Hkv
+    if qkv.dim() != 3 or qkv.shape[2] % heads:
+        raise ValueError(f"qkv must be [B, n, {heads} d]")
+    Q, K, V = _FusedNormRope.apply(
+        qkv.unflatten(2, (heads, qkv.shape[2] // heads)), Hq, Hkv, inv_freq,
+        q_weight, k_weight, eps, positions, pos0, interleaved)
+    return attention(Q, K, V, W, k, W_i=W_i, W_h=W_h, k_h=k_h,
+                     o_dtype=qkv.dtype if o_dtype is None else o_dtype)[0]

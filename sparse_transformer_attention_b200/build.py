@@ -42,11 +42,13 @@ def _nvcc() -> str:
 
 
 def sources() -> list:
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) +
+                  glob.glob(os.path.join(CSRC, "block", "*.cu")))
 
 
 def _deps() -> list:
     return glob.glob(os.path.join(CSRC, "*.cuh")) + \
+        glob.glob(os.path.join(CSRC, "block", "*.cuh")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 

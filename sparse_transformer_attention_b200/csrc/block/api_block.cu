@@ -1,0 +1,209 @@
+// C ABI of the operators around the attention: argument checks and dispatch.
+#include <limits.h>
+#include <stdint.h>
+
+#include "../../../include/condensate_attn.h"
+#include "block.cuh"
+
+namespace {
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+// A [B, n, heads] grid of rows: 16-byte aligned base and strides; a written
+// one must not fold several rows onto one address.
+ca_status check_rows(const ca_rows& r, int B, int n, int heads, int esize,
+                     bool written) {
+  const int64_t step = 16 / esize;
+  if (r.stride_b < 0 || r.stride_t < 0 || r.stride_h < 0)
+    return CA_ERR_INVALID_ARG;
+  if (!aligned16(r.data) || r.stride_b % step || r.stride_t % step ||
+      r.stride_h % step)
+    return CA_ERR_ALIGNMENT;
+  if (written && ((B > 1 && !r.stride_b) || (n > 1 && !r.stride_t) ||
+                  (heads > 1 && !r.stride_h)))
+    return CA_ERR_INVALID_ARG;
+  return CA_OK;
+}
+
+ca::Rows to_rows(const ca_rows& r) {
+  return {r.data, r.stride_b, r.stride_t, r.stride_h};
+}
+
+ca_status norm_rope_args(ca::NormRopeArgs& a, ca_dtype dtype, int B, int n,
+                         int Hq, int Hkv, int d, const ca_norm_rope* p) {
+  if (!p || B < 1 || n < 1 || Hq < 1 || Hkv < 1) return CA_ERR_INVALID_ARG;
+  if (Hq > (1 << 20) || Hkv > (1 << 20)) return CA_ERR_UNSUPPORTED;
+  if (dtype != CA_F32 && dtype != CA_BF16) return CA_ERR_UNSUPPORTED;
+  if (p->w_dtype != CA_F32 && p->w_dtype != CA_BF16) return CA_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return CA_ERR_UNSUPPORTED;
+  if (p->rot_dim < 0 || p->rot_dim > d) return CA_ERR_INVALID_ARG;
+  if (p->rot_dim % 16) return CA_ERR_UNSUPPORTED;
+  if (p->rot_dim > 0 && !p->inv_freq) return CA_ERR_INVALID_ARG;
+  if (!(p->eps >= 0.f) || p->eps > 1e30f) return CA_ERR_INVALID_ARG;
+  if (!p->positions && p->pos0 > INT_MAX - (n - 1)) return CA_ERR_INVALID_ARG;
+  if (!aligned4(p->inv_freq) || !aligned4(p->positions) ||
+      !aligned4(p->q_weight) || !aligned4(p->k_weight))
+    return CA_ERR_ALIGNMENT;
+  a = {};
+  a.B = B; a.n = n; a.Hq = Hq; a.Hkv = Hkv;
+  a.w[0] = p->q_weight; a.w[1] = p->k_weight;
+  a.w_bf16 = p->w_dtype == CA_BF16;
+  a.eps = p->eps;
+  a.inv_freq = p->inv_freq;
+  a.rot = p->rot_dim;
+  a.interleaved = p->interleaved != 0;
+  a.positions = p->positions;
+  a.pos0 = p->pos0;
+  return CA_OK;
+}
+
+bool group_ok(int Hq, int Hkv) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return false;
+  const int G = Hq / Hkv;
+  return G == 1 || G == 2 || G == 4 || G == 8;
+}
+
+ca_status from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return CA_OK;
+  return e == cudaErrorNotSupported ? CA_ERR_UNSUPPORTED : CA_ERR_CUDA;
+}
+
+// Largest Top-k of the backward pass: the prefill's.
+constexpr int kMaxK = 128;
+
+}  // namespace
+
+extern "C" {
+
+ca_status condensate_attn_norm_rope(const ca_rows* in, ca_dtype dtype, int B,
+                                    int n, int Hq, int Hkv, int d,
+                                    const ca_norm_rope* p, const ca_rows* out,
+                                    void* stream) {
+  if (!in || !out) return CA_ERR_INVALID_ARG;
+  ca::NormRopeArgs a;
+  ca_status st = norm_rope_args(a, dtype, B, n, Hq, Hkv, d, p);
+  if (st != CA_OK) return st;
+  const int es = dtype == CA_BF16 ? 2 : 4;
+  for (int i = 0; i < 3; ++i) {
+    if (!in[i].data != !out[i].data || (i == 0 && !in[i].data))
+      return CA_ERR_INVALID_ARG;
+    if (!in[i].data) continue;
+    const int heads = i == 0 ? Hq : Hkv;
+    if ((st = check_rows(in[i], B, n, heads, es, false)) != CA_OK ||
+        (st = check_rows(out[i], B, n, heads, es, true)) != CA_OK)
+      return st;
+    a.x[i] = to_rows(in[i]);
+    a.y[i] = to_rows(out[i]);
+  }
+  return from_cuda(
+      ca::norm_rope_launch(a, dtype == CA_BF16, d, (cudaStream_t)stream));
+}
+
+size_t condensate_attn_norm_rope_workspace_size(int d) {
+  if (d != 64 && d != 128) return 0;
+  return (size_t)ca::kNormRopeMaxCtas * 2 * d * 4;
+}
+
+ca_status condensate_attn_norm_rope_backward(
+    const ca_rows* grad_out, const ca_rows* in, ca_dtype dtype, int B, int n,
+    int Hq, int Hkv, int d, const ca_norm_rope* p, const ca_rows* grad_in,
+    void* grad_q_weight, void* grad_k_weight, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  if (!grad_out || !grad_in) return CA_ERR_INVALID_ARG;
+  ca::NormRopeArgs a;
+  ca_status st = norm_rope_args(a, dtype, B, n, Hq, Hkv, d, p);
+  if (st != CA_OK) return st;
+  const int es = dtype == CA_BF16 ? 2 : 4;
+  for (int i = 0; i < 3; ++i) {
+    if (!grad_out[i].data != !grad_in[i].data || (i == 0 && !grad_in[i].data))
+      return CA_ERR_INVALID_ARG;
+    if (!grad_in[i].data) continue;
+    const int heads = i == 0 ? Hq : Hkv;
+    if ((st = check_rows(grad_out[i], B, n, heads, es, false)) != CA_OK ||
+        (st = check_rows(grad_in[i], B, n, heads, es, true)) != CA_OK)
+      return st;
+    a.y[i] = to_rows(grad_out[i]);
+    a.dx[i] = to_rows(grad_in[i]);
+    if (i < 2 && a.w[i]) {  // the norm's gradient needs its input
+      if (!in || !in[i].data) return CA_ERR_INVALID_ARG;
+      if ((st = check_rows(in[i], B, n, heads, es, false)) != CA_OK) return st;
+      a.x[i] = to_rows(in[i]);
+    }
+  }
+  if (!a.dx[1].p) a.w[1] = nullptr;
+  if ((grad_q_weight && !a.w[0]) || (grad_k_weight && !a.w[1]))
+    return CA_ERR_INVALID_ARG;
+  if (!aligned4(grad_q_weight) || !aligned4(grad_k_weight))
+    return CA_ERR_ALIGNMENT;
+  if (grad_q_weight || grad_k_weight) {
+    if (!workspace ||
+        workspace_bytes < condensate_attn_norm_rope_workspace_size(d))
+      return CA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return CA_ERR_ALIGNMENT;
+    a.partial = (float*)workspace;
+    a.dw[0] = grad_q_weight;
+    a.dw[1] = grad_k_weight;
+  }
+  return from_cuda(ca::norm_rope_backward_launch(a, dtype == CA_BF16, d,
+                                                 (cudaStream_t)stream));
+}
+
+size_t condensate_attn_prefill_backward_workspace_size(
+    ca_dtype dtype, ca_dtype o_dtype, int B, int nq, int L, int Hq, int Hkv,
+    int d, int k) {
+  if (B < 1 || nq < 1 || L < nq || !group_ok(Hq, Hkv) || k < 0 || k > kMaxK ||
+      (d != 64 && d != 128) || (dtype != CA_F32 && dtype != CA_BF16) ||
+      (o_dtype != CA_F32 && o_dtype != CA_BF16))
+    return 0;
+  return ca::backward_workspace(dtype == CA_BF16, o_dtype == CA_BF16, B, nq, L,
+                                Hq, Hkv, d, k);
+}
+
+ca_status condensate_attn_prefill_backward(
+    const void* Q, const void* K, const void* V, ca_dtype dtype,
+    const void* dO, ca_dtype o_dtype, int B, int nq, int L, int Hq, int Hkv,
+    int d, int W, int k, const int32_t* W_i, const int32_t* W_h,
+    const int32_t* idx, const int32_t* idx_count, int C_max, void* dQ,
+    void* dK, void* dV, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  if (!workspace) return CA_ERR_WORKSPACE;
+  if (!Q || !K || !V || !dO || !idx || !idx_count || !dQ || !dK || !dV)
+    return CA_ERR_INVALID_ARG;
+  if (B < 1 || nq < 1 || L < nq || k < 0 || C_max < 1 || Hq < 1 || Hkv < 1 ||
+      Hq % Hkv != 0)
+    return CA_ERR_INVALID_ARG;
+  if (!W_i && !W_h) {
+    if (W < 1) return CA_ERR_INVALID_ARG;
+    long long need = 1LL + W + k;
+    if (need > L) need = L;
+    if (C_max < need) return CA_ERR_INVALID_ARG;
+  }
+  if ((dtype != CA_F32 && dtype != CA_BF16) ||
+      (o_dtype != CA_F32 && o_dtype != CA_BF16))
+    return CA_ERR_UNSUPPORTED;
+  if ((d != 64 && d != 128) || !group_ok(Hq, Hkv) || k > kMaxK)
+    return CA_ERR_UNSUPPORTED;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(dO) ||
+      !aligned16(idx) || !aligned16(idx_count) || !aligned16(dQ) ||
+      !aligned16(dK) || !aligned16(dV) || !aligned16(workspace) ||
+      !aligned4(W_i) || !aligned4(W_h))
+    return CA_ERR_ALIGNMENT;
+  const size_t need = condensate_attn_prefill_backward_workspace_size(
+      dtype, o_dtype, B, nq, L, Hq, Hkv, d, k);
+  if (need == 0) return CA_ERR_UNSUPPORTED;
+  if (workspace_bytes < need) return CA_ERR_WORKSPACE;
+  ca::BackwardArgs a;
+  a.Q = Q; a.K = K; a.V = V; a.dO = dO;
+  a.do_bf16 = o_dtype == CA_BF16;
+  a.B = B; a.nq = nq; a.L = L; a.p0 = L - nq;
+  a.Hq = Hq; a.Hkv = Hkv; a.W = W; a.k = k;
+  a.W_i = W_i; a.W_h = W_h;
+  a.idx = idx; a.idx_count = idx_count; a.C_max = C_max;
+  a.dQ = dQ; a.dK = dK; a.dV = dV;
+  a.status = (uint32_t*)workspace;
+  return from_cuda(ca::backward_launch(a, dtype == CA_BF16, d, workspace,
+                                       (cudaStream_t)stream));
+}
+
+}  // extern "C"
