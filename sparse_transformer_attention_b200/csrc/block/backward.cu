@@ -18,34 +18,17 @@
 // sum depends on timing: every order of addition is fixed by the inputs.
 #include "../launch.cuh"
 #include "../profile.cuh"
-#include "block.cuh"
+#include "backward.cuh"
 
 namespace ca {
 namespace {
 
-constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr float kLog2e = 1.4426950408889634f;
-
-// ------------------------------------------------------------- workspace
-// Entry e of a kv head: (q-head of its group, query row, slot), slot 0 the
-// anchor (when it lies outside the window), slots 1..k the Top-k positions
-// in the order of idx; unused slots hold key L, which sorts behind all keys.
-constexpr int kTile = 4096;   // entries per CTA of the sort
-constexpr int kRange = 128;   // sorted entries per warp of the listed pass
-
-struct Work {
-  int64_t rows;      // B * Hq * nq
-  int64_t per_head;  // entries of one kv head: G * nq * (k + 1)
-  int segs;          // B * Hkv
-  int tiles;         // sort tiles per segment
-  int ranges;        // listed-pass ranges per segment
-  int bits, passes;  // key bits; sort passes
-  size_t wmax, stats, pds, key[2], ent[2], hist, span, top, carry, total;
-};
+using namespace bwd;
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-bool plan(Work& w, int B, int nq, int L, int Hq, int Hkv, int d, int k) {
+bool plan(Work& w, bool planes, int B, int nq, int L, int Hq, int Hkv, int d,
+          int k) {
   w.rows = (int64_t)B * Hq * nq;
   w.segs = B * Hkv;
   const int64_t per = (int64_t)(Hq / Hkv) * nq * (k + 1);
@@ -58,6 +41,7 @@ bool plan(Work& w, int B, int nq, int L, int Hq, int Hkv, int d, int k) {
   w.bits = 1;
   while (((int64_t)1 << w.bits) <= L) ++w.bits;  // keys 0..L
   w.passes = (w.bits + 7) / 8;
+  w.digit = (w.bits + w.passes - 1) / w.passes;
   const size_t n = (size_t)w.segs * per;
   size_t at = kStatusBytes;
   auto take = [&](size_t bytes) {
@@ -66,6 +50,7 @@ bool plan(Work& w, int B, int nq, int L, int Hq, int Hkv, int d, int k) {
     return a;
   };
   w.wmax = take((size_t)B * 4);
+  w.lows = take((size_t)B * ((nq + kRowChunk - 1) / kRowChunk) * 4);
   w.stats = take((size_t)w.rows * 8);
   w.pds = take(n * 8);
   for (int i = 0; i < 2; ++i) {
@@ -73,62 +58,57 @@ bool plan(Work& w, int B, int nq, int L, int Hq, int Hkv, int d, int k) {
     w.ent[i] = take(n * 4);
   }
   w.hist = take((size_t)w.segs * 256 * w.tiles * 4);
+  w.totals = take((size_t)w.segs * 256 * 4);
   w.span = take((size_t)w.segs * L * 8);
   w.top = take((size_t)w.segs * L * 2 * d * 4);
   w.carry = take((size_t)w.segs * w.ranges * 2 * d * 4);
+  w.planes = take(planes ? (size_t)w.rows * d * 4 : 0);
   w.total = at;
   return true;
 }
 
-struct Args : BackwardArgs {
-  Work w;
-  int* wmax;       // [B] largest window of each batch row (W_i given)
-  float2* stats;   // [B, Hq, nq] log2-domain log-sum-exp, D
-  float2* pds;     // [entries] p, dS
-  uint32_t* key[2];
-  uint32_t* ent[2];
-  uint32_t* hist;  // [segs, 256, tiles]
-  int2* span;      // [segs, L] first and behind-last sorted entry of a key
-  float* top;      // [segs, L, 2, d] listed part of dK and dV
-  float* carry;    // [segs, ranges, 2, d] a range's share of the key that
-                   // began in an earlier range
-};
-
-// The window of query row r of head h: [lo, i].
-__device__ __forceinline__ int window_lo(const Args& a, int b, int h, int r,
-                                         bool report, int* w) {
-  *w = row_window(a.W_i, (int64_t)b * a.nq + r, a.W_h, h, a.W, a.L, a.status,
-                  report);
-  const int lo = a.p0 + r - *w + 1;
-  return lo > 0 ? lo : 0;
-}
-
-// Top-k entries of a row's index list: |C_i| less the anchor and the window.
-// A count that does not fit the window, k or C_max raises kErrCmax.
-__device__ __forceinline__ int listed_count(const Args& a, int64_t row, int i,
-                                            int lo, int w, bool report) {
-  const int c = __ldg(a.idx_count + row);
-  if (lo == 0) {
-    if (c != i + 1 && report) raise_flag(a.status, kErrCmax);
-    return 0;
+// Per batch row, the largest window; per chunk of rows, the lowest window
+// start: what lets the column pass skip rows that cannot reach its keys.
+__global__ void backward_windows(Args a) {
+  const int b = blockIdx.y, chunks = gridDim.x;
+  __shared__ int s_w[2], s_lo[2];
+  const int r = blockIdx.x * kRowChunk + threadIdx.x;  // kRowChunk threads
+  int w = 1, lo = 0x7FFFFFFF;
+  if (r < a.nq) {
+    w = min(max(a.W_i[(int64_t)b * a.nq + r], 1), a.L);
+    lo = max(a.p0 + r - w + 1, 0);
   }
-  int m = c - 1 - w;
-  const int most = min(a.k, a.C_max - 1);
-  if (m < 0 || m > most) {
-    if (report) raise_flag(a.status, kErrCmax);
-    m = m < 0 ? 0 : most;
-  }
-  return m;
-}
-
-__global__ void backward_window_max(Args a) {
-  const int b = blockIdx.y;
-  const int r = blockIdx.x * blockDim.x + threadIdx.x;
-  int w = r < a.nq ? min(max(a.W_i[(int64_t)b * a.nq + r], 1), a.L) : 1;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
+  for (int off = 16; off > 0; off >>= 1) {
     w = max(w, __shfl_xor_sync(kAll, w, off));
-  if ((threadIdx.x & 31) == 0) atomicMax(a.wmax + b, w);
+    lo = min(lo, __shfl_xor_sync(kAll, lo, off));
+  }
+  if ((threadIdx.x & 31) == 0) {
+    s_w[threadIdx.x >> 5] = w;
+    s_lo[threadIdx.x >> 5] = lo;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    atomicMax(a.wmax + b, max(s_w[0], s_w[1]));
+    a.lows[b * chunks + blockIdx.x] = min(s_lo[0], s_lo[1]);
+  }
+}
+
+// An fp32 dO as two bf16 planes (see Args::g).
+__global__ void __launch_bounds__(256)
+backward_split(const float4* x, uint2* hi, uint2* lo, int64_t n4) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const float4 v = x[i];
+  const float f[4] = {v.x, v.y, v.z, v.w};
+  __nv_bfloat16 h[4], l[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    h[c] = __float2bfloat16_rn(f[c]);
+    l[c] = __float2bfloat16_rn(f[c] - __bfloat162float(h[c]));
+  }
+  hi[i] = *reinterpret_cast<const uint2*>(h);
+  lo[i] = *reinterpret_cast<const uint2*>(l);
 }
 
 // ---------------------------------------------------------------- row pass
@@ -273,126 +253,6 @@ __global__ void __launch_bounds__(kRowWarps * 32) backward_rows(Args a) {
       key[t] = (uint32_t)a.L;
     }
     a.pds[row * (a.k + 1) + t] = o;
-  }
-}
-
-// -------------------------------------------------------------------- sort
-// Stable least-significant-digit sort of each kv head's entries by key.
-// A CTA counts (sort_count) or places (sort_place) a tile of kTile entries;
-// counts are laid out digit-major so that one exclusive scan per kv head
-// (sort_scan) gives each (digit, tile) its first place.
-constexpr int kSortThreads = 256;
-
-__global__ void __launch_bounds__(kSortThreads)
-sort_count(Args a, const uint32_t* key, int shift) {
-  __shared__ uint32_t cnt[256];
-  const int64_t base = (int64_t)blockIdx.y * a.w.per_head;
-  const int64_t e0 = (int64_t)blockIdx.x * kTile;
-  const int n = (int)min((int64_t)kTile, a.w.per_head - e0);
-  cnt[threadIdx.x] = 0;
-  __syncthreads();
-  for (int t = threadIdx.x; t < n; t += kSortThreads)
-    atomicAdd(&cnt[(key[base + e0 + t] >> shift) & 255u], 1u);
-  __syncthreads();
-  a.hist[((size_t)blockIdx.y * 256 + threadIdx.x) * a.w.tiles + blockIdx.x] =
-      cnt[threadIdx.x];
-}
-
-__global__ void __launch_bounds__(1024) sort_scan(Args a) {
-  __shared__ uint32_t s_warp[32];
-  __shared__ uint32_t s_carry;
-  const int n = 256 * a.w.tiles;
-  uint32_t* h = a.hist + (size_t)blockIdx.x * n;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  if (threadIdx.x == 0) s_carry = 0;
-  __syncthreads();
-  for (int c0 = 0; c0 < n; c0 += 1024) {
-    const int c = c0 + threadIdx.x;
-    const uint32_t v = c < n ? h[c] : 0u;
-    uint32_t x = v;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t y = __shfl_up_sync(kAll, x, off);
-      if (lane >= off) x += y;
-    }
-    if (lane == 31) s_warp[wid] = x;
-    __syncthreads();
-    if (wid == 0) {
-      uint32_t y = s_warp[lane];
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t z = __shfl_up_sync(kAll, y, off);
-        if (lane >= off) y += z;
-      }
-      s_warp[lane] = y;
-    }
-    __syncthreads();
-    const uint32_t before = s_carry + (wid ? s_warp[wid - 1] : 0u);
-    if (c < n) h[c] = before + x - v;
-    __syncthreads();
-    if (threadIdx.x == 0) s_carry += s_warp[31];
-    __syncthreads();
-  }
-}
-
-// Places a tile: every warp ranks its run of the tile's entries in order
-// (equal digits of a step by lane, earlier steps by a running count), then
-// the warps' counts are chained and each entry goes to its place.
-__global__ void __launch_bounds__(kSortThreads)
-sort_place(Args a, const uint32_t* key, const uint32_t* ent, uint32_t* key_out,
-           uint32_t* ent_out, int shift) {
-  constexpr int kW = kSortThreads / 32;
-  constexpr int kSteps = kTile / kSortThreads;  // steps of 32 per warp
-  __shared__ uint32_t cnt[kW][256];
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int64_t base = (int64_t)blockIdx.y * a.w.per_head;
-  const int64_t e0 = (int64_t)blockIdx.x * kTile + wid * (32 * kSteps);
-  for (int c = threadIdx.x; c < kW * 256; c += kSortThreads)
-    (&cnt[0][0])[c] = 0;
-  __syncthreads();
-  uint32_t kv[kSteps], rank[kSteps];
-#pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int64_t e = e0 + u * 32 + lane;
-    kv[u] = e < a.w.per_head ? key[base + e] : 0xFFFFFFFFu;
-  }
-#pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const bool live = e0 + u * 32 + lane < a.w.per_head;
-    // dead lanes are a tail of the last steps: a digit of their own
-    const uint32_t dg = live ? (kv[u] >> shift) & 255u : 256u;
-    const uint32_t same = __match_any_sync(kAll, dg);
-    const uint32_t lower = same & ((1u << lane) - 1u);
-    uint32_t before = 0;
-    if (live) before = cnt[wid][dg];
-    __syncwarp();
-    if (live && lower == 0) cnt[wid][dg] = before + __popc(same);
-    __syncwarp();
-    rank[u] = before + __popc(lower);
-  }
-  __syncthreads();
-  {
-    const int dg = threadIdx.x;  // kSortThreads = 256 digits
-    uint32_t at =
-        a.hist[((size_t)blockIdx.y * 256 + dg) * a.w.tiles + blockIdx.x];
-#pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      const uint32_t c = cnt[w][dg];
-      cnt[w][dg] = at;
-      at += c;
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int64_t e = e0 + u * 32 + lane;
-    if (e < a.w.per_head) {
-      const uint32_t at = cnt[wid][(kv[u] >> shift) & 255u] + rank[u];
-      if (in_bounds(at < a.w.per_head, a.status)) {
-        key_out[base + at] = kv[u];
-        ent_out[base + at] = ent ? ent[base + e] : (uint32_t)e;
-      }
-    }
   }
 }
 
@@ -561,57 +421,66 @@ cudaError_t run(const char* name, F* kern, dim3 grid, int threads, size_t smem,
 
 template <typename T, typename TD, int D>
 cudaError_t launch_as(Args a, cudaStream_t s) {
+  constexpr bool kMma = sizeof(T) == 2;  // bf16: the tensor-core kernels
   const Work& w = a.w;
-  cudaError_t e;
-  if (a.W_i) {
-    e = run("backward_window_max", backward_window_max,
-            dim3((a.nq + 255) / 256, a.B), 256, 0, s, a);
-    if (e != cudaSuccess) return e;
-  }
-  e = run("backward_rows", backward_rows<T, TD, D>,
-          dim3((unsigned)((w.rows + kRowWarps - 1) / kRowWarps)),
-          kRowWarps * 32, (size_t)kRowWarps * (a.k + 1) * 8, s, a);
+  cudaError_t e = cudaSuccess;
+  if (a.W_i)
+    e = run("backward_windows", backward_windows,
+            dim3((a.nq + kRowChunk - 1) / kRowChunk, a.B), kRowChunk, 0, s, a);
   if (e != cudaSuccess) return e;
-  int from = 0;
-  for (int p = 0; p < w.passes; ++p) {
-    const dim3 grid(w.tiles, w.segs);
-    const uint32_t* ent = p ? a.ent[from] : nullptr;
-    if ((e = run("sort_count", sort_count, grid, kSortThreads, 0, s, a,
-                 (const uint32_t*)a.key[from], 8 * p)) != cudaSuccess ||
-        (e = run("sort_scan", sort_scan, dim3(w.segs), 1024, 0, s, a)) !=
-            cudaSuccess ||
-        (e = run("sort_place", sort_place, grid, kSortThreads, 0, s, a,
-                 (const uint32_t*)a.key[from], ent, a.key[from ^ 1],
-                 a.ent[from ^ 1], 8 * p)) != cudaSuccess)
-      return e;
-    from ^= 1;
+  if constexpr (kMma) {
+    if (a.do_bf16) {
+      a.g[0] = reinterpret_cast<const __nv_bfloat16*>(a.dO);
+      a.g[1] = nullptr;
+    } else {
+      const int64_t n4 = w.rows * D / 4;
+      e = run("backward_split", backward_split,
+              dim3((unsigned)((n4 + 255) / 256)), 256, 0, s,
+              (const float4*)a.dO, (uint2*)a.g[0], (uint2*)a.g[1], n4);
+      if (e != cudaSuccess) return e;
+    }
+    e = rows_mma_launch(a, D, s);
+  } else {
+    e = run("backward_rows", backward_rows<T, TD, D>,
+            dim3((unsigned)((w.rows + kRowWarps - 1) / kRowWarps)),
+            kRowWarps * 32, (size_t)kRowWarps * (a.k + 1) * 8, s, a);
   }
+  if (e != cudaSuccess) return e;
+  int last;
+  if ((e = sort_launch(a, &last, s)) != cudaSuccess) return e;
   e = cudaMemsetAsync(a.span, 0, (size_t)w.segs * a.L * 8, s);
   if (e != cudaSuccess) return e;
-  e = run("backward_listed", backward_listed<T, TD, D>,
-          dim3((w.ranges + 7) / 8, w.segs), 256, 0, s, a,
-          (const uint32_t*)a.key[from], (const uint32_t*)a.ent[from]);
-  if (e != cudaSuccess) return e;
-  return run("backward_columns", backward_columns<T, TD, D>,
-             dim3((unsigned)(((int64_t)w.segs * a.L + 7) / 8)), 256, 0, s, a);
+  const uint32_t *keys = a.key[last], *ents = a.ent[last];
+  if constexpr (kMma) {
+    if ((e = listed_mma_launch(a, D, keys, ents, s)) != cudaSuccess) return e;
+    return columns_mma_launch(a, D, s);
+  } else {
+    e = run("backward_listed", backward_listed<T, TD, D>,
+            dim3((w.ranges + 7) / 8, w.segs), 256, 0, s, a, keys, ents);
+    if (e != cudaSuccess) return e;
+    return run("backward_columns", backward_columns<T, TD, D>,
+               dim3((unsigned)(((int64_t)w.segs * a.L + 7) / 8)), 256, 0, s,
+               a);
+  }
 }
 
 }  // namespace
 
-size_t backward_workspace(bool, bool, int B, int nq, int L, int Hq, int Hkv,
-                          int d, int k) {
+size_t backward_workspace(bool bf16, bool do_bf16, int B, int nq, int L,
+                          int Hq, int Hkv, int d, int k) {
   Work w;
-  return plan(w, B, nq, L, Hq, Hkv, d, k) ? w.total : 0;
+  return plan(w, bf16 && !do_bf16, B, nq, L, Hq, Hkv, d, k) ? w.total : 0;
 }
 
 cudaError_t backward_launch(const BackwardArgs& in, bool bf16, int d, void* ws,
                             cudaStream_t s) {
   Args a;
   static_cast<BackwardArgs&>(a) = in;
-  if (!plan(a.w, a.B, a.nq, a.L, a.Hq, a.Hkv, d, a.k))
+  if (!plan(a.w, bf16 && !a.do_bf16, a.B, a.nq, a.L, a.Hq, a.Hkv, d, a.k))
     return cudaErrorNotSupported;
   char* p = (char*)ws;
   a.wmax = (int*)(p + a.w.wmax);
+  a.lows = (int*)(p + a.w.lows);
   a.stats = (float2*)(p + a.w.stats);
   a.pds = (float2*)(p + a.w.pds);
   for (int i = 0; i < 2; ++i) {
@@ -619,19 +488,18 @@ cudaError_t backward_launch(const BackwardArgs& in, bool bf16, int d, void* ws,
     a.ent[i] = (uint32_t*)(p + a.w.ent[i]);
   }
   a.hist = (uint32_t*)(p + a.w.hist);
+  a.totals = (uint32_t*)(p + a.w.totals);
   a.span = (int2*)(p + a.w.span);
   a.top = (float*)(p + a.w.top);
   a.carry = (float*)(p + a.w.carry);
+  a.g[0] = (const __nv_bfloat16*)(p + a.w.planes);
+  a.g[1] = a.g[0] + a.w.rows * d;
   // the status area and, behind it, the window maxima
-  cudaError_t e = cudaMemsetAsync(ws, 0, a.w.stats, s);
+  cudaError_t e = cudaMemsetAsync(ws, 0, a.w.lows, s);
   if (e != cudaSuccess) return e;
   using bf = __nv_bfloat16;
   if (bf16) {
-    if (a.do_bf16)
-      return d == 64 ? launch_as<bf, bf, 64>(a, s)
-                     : launch_as<bf, bf, 128>(a, s);
-    return d == 64 ? launch_as<bf, float, 64>(a, s)
-                   : launch_as<bf, float, 128>(a, s);
+    return d == 64 ? launch_as<bf, bf, 64>(a, s) : launch_as<bf, bf, 128>(a, s);
   }
   if (a.do_bf16)
     return d == 64 ? launch_as<float, bf, 64>(a, s)

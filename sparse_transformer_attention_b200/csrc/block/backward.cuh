@@ -1,0 +1,86 @@
+// Workspace, arguments and row helpers shared by the kernels of the prefill's
+// backward pass (internal).
+#pragma once
+
+#include "block.cuh"
+
+namespace ca {
+namespace bwd {
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ------------------------------------------------------------- workspace
+// Entry e of a kv head: (q-head of its group, query row, slot), slot 0 the
+// anchor (when it lies outside the window), slots 1..k the Top-k positions
+// in the order of idx; unused slots hold key L, which sorts behind all keys.
+constexpr int kTile = 4096;   // entries per CTA of the sort
+constexpr int kRange = 128;   // sorted entries per warp of the listed pass
+constexpr int kRowChunk = 64; // query rows staged at a time by the columns
+
+struct Work {
+  int64_t rows;      // B * Hq * nq
+  int64_t per_head;  // entries of one kv head: G * nq * (k + 1)
+  int segs;          // B * Hkv
+  int tiles;         // sort tiles per segment
+  int ranges;        // listed-pass ranges per segment
+  int bits, passes, digit;  // key bits; sort passes; bits of each
+  size_t wmax, lows, stats, pds, key[2], ent[2], hist, totals, span, top,
+      carry, planes, total;
+};
+
+struct Args : BackwardArgs {
+  Work w;
+  int* wmax;       // [B] largest window of each batch row (W_i given)
+  int* lows;       // [B, chunks] lowest window start of each kRowChunk rows
+  float2* stats;   // [B, Hq, nq] log2-domain log-sum-exp, D
+  float2* pds;     // [entries] p, dS
+  uint32_t* key[2];
+  uint32_t* ent[2];
+  uint32_t* hist;    // [segs, 256, tiles] entries of a tile by digit
+  uint32_t* totals;  // [segs, 256] entries by digit
+  int2* span;      // [segs, L] first and behind-last sorted entry of a key
+  float* top;      // [segs, L, 2, d] listed part of dK and dV
+  float* carry;    // [segs, ranges, 2, d] a range's share of the key that
+                   // began in an earlier range
+  // dO in bf16: dO itself, or an fp32 dO as two planes, dO = hi + lo up to
+  // 2^-16 of its value
+  const __nv_bfloat16* g[2];
+};
+
+// The window of query row r of head h: [lo, i].
+__device__ __forceinline__ int window_lo(const Args& a, int b, int h, int r,
+                                         bool report, int* w) {
+  *w = row_window(a.W_i, (int64_t)b * a.nq + r, a.W_h, h, a.W, a.L, a.status,
+                  report);
+  const int lo = a.p0 + r - *w + 1;
+  return lo > 0 ? lo : 0;
+}
+
+// Top-k entries of a row's index list: |C_i| less the anchor and the window.
+// A count that does not fit the window, k or C_max raises kErrCmax.
+__device__ __forceinline__ int listed_count(const Args& a, int64_t row, int i,
+                                            int lo, int w, bool report) {
+  const int c = __ldg(a.idx_count + row);
+  if (lo == 0) {
+    if (c != i + 1 && report) raise_flag(a.status, kErrCmax);
+    return 0;
+  }
+  const int64_t m = (int64_t)c - 1 - w;
+  const int most = min(a.k, a.C_max - 1);
+  if ((m < 0 || m > most) && report) raise_flag(a.status, kErrCmax);
+  return m < 0 ? 0 : m > most ? most : (int)m;
+}
+
+// Key order of a kv head's entries: sorts (key, entry) pairs by key, equal
+// keys in entry order, starting from a.key[0] (entry numbers implied).  The
+// result is in a.key[*last], a.ent[*last].
+cudaError_t sort_launch(const Args& a, int* last, cudaStream_t s);
+// The row pass, the listed pass and the column pass on tensor cores (bf16).
+cudaError_t rows_mma_launch(const Args& a, int d, cudaStream_t s);
+cudaError_t listed_mma_launch(const Args& a, int d, const uint32_t* keys,
+                              const uint32_t* ents, cudaStream_t s);
+cudaError_t columns_mma_launch(const Args& a, int d, cudaStream_t s);
+
+}  // namespace bwd
+}  // namespace ca

@@ -1,0 +1,985 @@
+// The prefill's backward pass for bf16 on matrix instructions.  All products
+// run as m16n8k16 bf16 with fp32 sums.  Operands that are not inputs (p, dS,
+// e dP) enter in two bf16 parts, hi + lo, so that they keep 16 bits: with one
+// part the gradients' error would be half as large again as that of the
+// rounding to bf16 at the end.
+//
+// The work per (row, key) pair is small and most pairs are gathered, so what
+// bounds these kernels is reading rows from L2 and issuing instructions, not
+// the tensor pipe; the layouts below keep both low.
+#include "../launch.cuh"
+#include "../profile.cuh"
+#include "backward.cuh"
+
+namespace ca {
+namespace bwd {
+namespace {
+
+using bf = __nv_bfloat16;
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1,
+                                    uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+      "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 tile of 16-bit elements held one row per four
+// lanes, two elements per lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void* p) {
+  asm volatile(
+      "ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"((uint32_t)__cvta_generic_to_shared(p))
+      : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], const void* p) {
+  asm volatile(
+      "ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"((uint32_t)__cvta_generic_to_shared(p))
+      : "memory");
+}
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+// Two values as the hi and lo parts of a bf16 pair each.
+__device__ __forceinline__ void split2(float x, float y, uint32_t* hi,
+                                       uint32_t* lo) {
+  *hi = pack2(x, y);
+  *lo = pack2(x - bf16lo(*hi), y - bf16hi(*hi));
+}
+
+// ---------------------------------------------------------------- row pass
+// A CTA owns 64 query rows of one head, a warp 16.  In order:
+//   1. the window's and the anchor's scores and dP: running (max, sum e,
+//      sum e dP) of each row;
+//   2. row by row, the Top-k: 16 gathered K and V rows at a time are the A
+//      operand of a product with q and dO (every column of B the same), so
+//      the score of key r lies in the lanes that hold its row.  The sums
+//      A = sum e dP k and Bk = sum e k take the same K registers, transposed
+//      in place, against a B operand whose columns are e dP and e in two
+//      parts each.  So a gathered row is read once, and dQ's listed part
+//      (A - D Bk) / l follows when the row's sums are complete;
+//   3. the window and the anchor again, now with the final log-sum-exp and
+//      D: dS, and dQ's window part.
+// The window is 5 blocks of 16 x 16 per 16 rows at W = 64, so computing its
+// scores twice costs less than keeping a second accumulator.
+constexpr int kRowWarps = 4;
+
+template <int D>
+struct RowSmem {
+  static constexpr int CK = 64;         // keys staged at a time
+  static constexpr int RS = D * 2 + 16; // padded row (bytes)
+  static constexpr size_t stage = (size_t)2 * CK * RS;  // K and V
+  static size_t per_warp(int k) {
+    const int kk = (k + 15) / 16 * 16;
+    return (size_t)16 * D * 4 + 4 * 16 * 4 + (size_t)kk * 8 +
+           (size_t)16 * kk * 4;
+  }
+  static size_t bytes(int k) { return stage + kRowWarps * per_warp(k); }
+};
+
+template <int D, int NP>
+__global__ void __launch_bounds__(kRowWarps * 32)
+backward_rows_mma(Args a, int ntile) {
+  using SM = RowSmem<D>;
+  constexpr int RS = SM::RS, CK = SM::CK;
+  constexpr int KS = D / 16;  // steps of a product over the head dimension
+  constexpr int NT = D / 8;   // its 8-wide tiles
+  constexpr int NC = D / 32;  // 64-byte pieces of a row
+  extern __shared__ __align__(16) unsigned char g_smem[];
+  __shared__ int s_kmin, s_any;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int gr = lane >> 2, tq = lane & 3;
+  const int k = a.k, kk = (k + 15) / 16 * 16;
+  const int nq = a.nq, L = a.L;
+  const int bh = blockIdx.x / ntile;
+  const int r0 = (blockIdx.x % ntile) * 64;
+  const int b = bh / a.Hq, h = bh % a.Hq;
+  const int seg = b * a.Hkv + h / (a.Hq / a.Hkv);
+  const int i0 = r0 + wid * 16;  // the warp's first row
+  const int64_t rowbase = (int64_t)bh * nq;
+  const bf* Qg = reinterpret_cast<const bf*>(a.Q) + rowbase * D;
+  const bf* Kg = reinterpret_cast<const bf*>(a.K) + (int64_t)seg * L * D;
+  const bf* Vg = reinterpret_cast<const bf*>(a.V) + (int64_t)seg * L * D;
+  unsigned char* sK = g_smem;
+  unsigned char* sV = g_smem + (size_t)CK * RS;
+  float* s_dq = reinterpret_cast<float*>(
+      g_smem + SM::stage +
+      (size_t)wid * ((size_t)16 * D * 4 + 4 * 16 * 4 + (size_t)kk * 8 +
+                     (size_t)16 * kk * 4));
+  float* s_m = s_dq + 16 * D;  // running maximum, then the log-sum-exp
+  float* s_l = s_m + 16;
+  float* s_E = s_l + 16;       // sum e dP, then D
+  int* s_top = reinterpret_cast<int*>(s_E + 16);  // Top-k entries of a row
+  float2* s_xd = reinterpret_cast<float2*>(s_top + 16);  // one row's (x, dP)
+  int* s_idx = reinterpret_cast<int*>(s_xd + kk);
+  const float sl2 = kLog2e / sqrtf((float)D), sc = 1.f / sqrtf((float)D);
+
+  if (threadIdx.x == 0) {
+    s_kmin = 0x7FFFFFFF;
+    s_any = 0;
+  }
+  __syncthreads();
+
+  // this lane's two rows of the warp's 16 in the window products
+  const bool wlive = i0 < nq;
+  const int ra = i0 + gr, rb = ra + 8;
+  const bool va = ra < nq, vb = rb < nq;
+  const int ca = min(ra, nq - 1), cb = min(rb, nq - 1);
+  const int ia = a.p0 + ca, ib = a.p0 + cb;
+  int wa, wb;
+  const int loa = window_lo(a, b, h, ca, va && tq == 0, &wa);
+  const int lob = window_lo(a, b, h, cb, vb && tq == 0, &wb);
+  int kmin = min(loa, lob);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    kmin = min(kmin, __shfl_xor_sync(kAll, kmin, off));
+  const int kmax = a.p0 + min(i0 + 15, nq - 1);
+  const bool anchors = __any_sync(kAll, (va && loa > 0) || (vb && lob > 0));
+  if (wlive && lane == 0) {
+    atomicMin(&s_kmin, kmin);
+    if (anchors) s_any = 1;
+  }
+
+  // the Top-k positions of the warp's rows: checked, kept, and written as
+  // the entries' sort keys
+#pragma unroll 1
+  for (int rr = 0; rr < 16 && i0 + rr < nq; ++rr) {
+    const int64_t row = rowbase + i0 + rr;
+    const int i = a.p0 + i0 + rr;
+    int w;
+    const int lo = window_lo(a, b, h, i0 + rr, false, &w);
+    const int m = listed_count(a, row, i, lo, w, lane == 0);
+    if (lane == 0) s_top[rr] = m;
+    uint32_t* key = a.key[0] + row * (k + 1);
+    const int32_t* ix = a.idx + row * a.C_max;
+    if (lane == 0) key[0] = lo > 0 ? 0u : (uint32_t)L;
+    for (int t = lane; t < k; t += 32) {
+      int j = -1;
+      if (t < m) {
+        j = __ldg(ix + 1 + t);
+        if (j < 1 || j > i - w) {  // not a candidate of this row
+          raise_flag(a.status, kErrCmax);
+          j = -1;
+        }
+      }
+      s_idx[rr * kk + t] = j;
+      key[1 + t] = j < 0 ? (uint32_t)L : (uint32_t)j;
+    }
+  }
+  __syncthreads();
+  const int cs0 = s_kmin & ~15;
+  const int kmax_c = a.p0 + min(r0 + 63, nq - 1);
+  const int nch = (kmax_c - cs0) / CK + 1;
+  const int m0 = s_any ? -1 : 0;  // chunk -1: the anchor's 16 keys
+
+  auto stage = [&](int m) {
+    const int cs = m < 0 ? 0 : cs0 + m * CK;
+    const int rows = m < 0 ? 16 : min(CK, kmax_c + 1 - cs);
+    constexpr int kPieces = D * 2 / 16;
+    for (int e = threadIdx.x; e < ((rows + 15) & ~15) * kPieces;
+         e += kRowWarps * 32) {
+      const int rr = e / kPieces, pc = e % kPieces;
+      const int j = min(cs + rr, L - 1);  // rows past the cache: any valid
+      cp_async16(sK + rr * RS + pc * 16, Kg + (size_t)j * D + pc * 8);
+      cp_async16(sV + rr * RS + pc * 16, Vg + (size_t)j * D + pc * 8);
+    }
+    cp_async_wait_all();
+  };
+  // scores (log2 units, masked to -inf) and dP of the 16 x 16 block of keys
+  // kb.. (at place kl of the staged chunk), as two accumulators of 8 keys
+  auto block = [&](const uint32_t (&qa)[KS][4], const uint32_t (&ga)[NP][KS][4],
+                   int kb, int kl, bool anchor, float (&x)[2][4],
+                   float (&dp)[2][4]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[t][c] = dp[t][c] = 0.f;
+    const int lr = kl + (lane & 7) + ((lane >> 4) << 3);
+    const int lc = ((lane >> 3) & 1) * 16;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      uint32_t f[4];
+      ldsm4(f, sK + lr * RS + ks * 32 + lc);
+      mma(x[0], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], f[0], f[1]);
+      mma(x[1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], f[2], f[3]);
+    }
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      uint32_t f[4];
+      ldsm4(f, sV + lr * RS + ks * 32 + lc);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        mma(dp[0], ga[p][ks][0], ga[p][ks][1], ga[p][ks][2], ga[p][ks][3],
+            f[0], f[1]);
+        mma(dp[1], ga[p][ks][0], ga[p][ks][1], ga[p][ks][2], ga[p][ks][3],
+            f[2], f[3]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int j = kb + 8 * t + 2 * tq + (c & 1);
+        const bool ok = c < 2
+            ? va && (anchor ? j == 0 && loa > 0 : j >= loa && j <= ia)
+            : vb && (anchor ? j == 0 && lob > 0 : j >= lob && j <= ib);
+        x[t][c] = ok ? x[t][c] * sl2 : -INFINITY;
+      }
+  };
+  auto fragments = [&](uint32_t (&qa)[KS][4], uint32_t (&ga)[NP][KS][4]) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int64_t at = (int64_t)((c & 1) ? cb : ca) * D + 16 * ks +
+                           2 * tq + (c >= 2 ? 8 : 0);
+        qa[ks][c] = __ldg(reinterpret_cast<const uint32_t*>(Qg + at));
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          ga[p][ks][c] = __ldg(
+              reinterpret_cast<const uint32_t*>(a.g[p] + rowbase * D + at));
+      }
+  };
+
+  // ---- 1: window and anchor, running sums
+  {
+    uint32_t qa[KS][4], ga[NP][KS][4];
+    fragments(qa, ga);
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, E[2] = {0.f, 0.f};
+#pragma unroll 1
+    for (int ch = m0; ch < nch; ++ch) {
+      stage(ch);
+      __syncthreads();
+      const int cs = ch < 0 ? 0 : cs0 + ch * CK;
+      const int jlo = ch < 0 ? 0 : max(cs, kmin & ~15);
+      const int jhi = ch < 0 ? (anchors ? 0 : -1) : min(cs + CK - 1, kmax);
+#pragma unroll 1
+      for (int kb = jlo; wlive && kb <= jhi; kb += 16) {
+        float x[2][4], dp[2][4];
+        block(qa, ga, kb, kb - cs, ch < 0, x, dp);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float mx = fmaxf(fmaxf(x[0][2 * u], x[0][2 * u + 1]),
+                                 fmaxf(x[1][2 * u], x[1][2 * u + 1]));
+          if (mx > m[u]) {
+            const float f = exp2f(m[u] - mx);
+            l[u] *= f;
+            E[u] *= f;
+            m[u] = mx;
+          }
+          if (m[u] == -INFINITY) continue;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float e = exp2f(x[t][2 * u + c] - m[u]);
+              l[u] += e;
+              E[u] = fmaf(e, dp[t][2 * u + c], E[u]);
+            }
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float mx = m[u];
+      mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
+      const float f = m[u] == -INFINITY ? 0.f : exp2f(m[u] - mx);
+      float ll = l[u] * f, EE = E[u] * f;
+      ll += __shfl_xor_sync(kAll, ll, 1);
+      EE += __shfl_xor_sync(kAll, EE, 1);
+      ll += __shfl_xor_sync(kAll, ll, 2);
+      EE += __shfl_xor_sync(kAll, EE, 2);
+      if (tq == 0) {
+        s_m[gr + 8 * u] = mx;
+        s_l[gr + 8 * u] = ll;
+        s_E[gr + 8 * u] = EE;
+      }
+    }
+    __syncwarp();
+  }
+
+  // ---- 2: the Top-k, row by row
+#pragma unroll 1
+  for (int rr = 0; rr < 16 && i0 + rr < nq; ++rr) {
+    const int64_t row = rowbase + i0 + rr;
+    const int mt = s_top[rr];
+    float m = s_m[rr], l0 = s_l[rr], E0 = s_E[rr];  // window and anchor
+    float l = 0.f, E = 0.f;  // this lane's keys
+    uint4 qv[NC], gv[NP][NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int64_t at = row * D + 32 * c + 8 * tq;
+      qv[c] = __ldg(reinterpret_cast<const uint4*>(
+          reinterpret_cast<const bf*>(a.Q) + at));
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        gv[p][c] = __ldg(reinterpret_cast<const uint4*>(a.g[p] + at));
+    }
+    float acc[2 * NC][4];
+#pragma unroll
+    for (int t = 0; t < 2 * NC; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[t][c] = 0.f;
+#pragma unroll 1
+    for (int g0 = 0; g0 < mt; g0 += 16) {
+      const int ja = g0 + gr < mt ? s_idx[rr * kk + g0 + gr] : -1;
+      const int jb = g0 + gr + 8 < mt ? s_idx[rr * kk + g0 + gr + 8] : -1;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      uint4 ka[NC], kb[NC], vva[NC], vvb[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int64_t pa = (int64_t)ja * D + 32 * c + 8 * tq;
+        const int64_t pb = (int64_t)jb * D + 32 * c + 8 * tq;
+        ka[c] = ja >= 0 ? __ldg(reinterpret_cast<const uint4*>(Kg + pa)) : zero;
+        kb[c] = jb >= 0 ? __ldg(reinterpret_cast<const uint4*>(Kg + pb)) : zero;
+        vva[c] = ja >= 0 ? __ldg(reinterpret_cast<const uint4*>(Vg + pa)) : zero;
+        vvb[c] = jb >= 0 ? __ldg(reinterpret_cast<const uint4*>(Vg + pb)) : zero;
+      }
+      float x[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        mma(x, ka[c].x, kb[c].x, ka[c].y, kb[c].y, qv[c].x, qv[c].y);
+        mma(x, ka[c].z, kb[c].z, ka[c].w, kb[c].w, qv[c].z, qv[c].w);
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          mma(dp, vva[c].x, vvb[c].x, vva[c].y, vvb[c].y, gv[p][c].x,
+              gv[p][c].y);
+          mma(dp, vva[c].z, vvb[c].z, vva[c].w, vvb[c].w, gv[p][c].z,
+              gv[p][c].w);
+        }
+      // keys gr and gr + 8, the same in all four lanes of a row
+      const float xa = ja >= 0 ? x[0] * sl2 : -INFINITY;
+      const float xb = jb >= 0 ? x[2] * sl2 : -INFINITY;
+      float mx = fmaxf(xa, xb);
+#pragma unroll
+      for (int off = 4; off <= 16; off <<= 1)
+        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, off));
+      if (mx > m) {  // the same for the whole warp
+        const float f = exp2f(m - mx);
+        l0 *= f;
+        E0 *= f;
+        l *= f;
+        E *= f;
+#pragma unroll
+        for (int t = 0; t < 2 * NC; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[t][c] *= f;
+        m = mx;
+      }
+      const float ea = exp2f(xa - m), eb = exp2f(xb - m);
+      l += ea + eb;
+      E = fmaf(ea, dp[0], fmaf(eb, dp[2], E));
+      if (tq == 0) {
+        s_xd[g0 + gr] = make_float2(xa, dp[0]);
+        s_xd[g0 + gr + 8] = make_float2(xb, dp[2]);
+      }
+      // B: columns 0, 1 = e dP (hi, lo), 2, 3 = e (hi, lo), 4..7 zero; this
+      // lane's are keys 2 tq, 2 tq + 1, and those + 8, of column gr
+      const float sa = (tq & 1) ? ea : ea * dp[0];
+      const float sb = (tq & 1) ? eb : eb * dp[2];
+      const int src = 8 * tq + ((gr >> 1) & 1);
+      float b00 = __shfl_sync(kAll, sa, src), b01 = __shfl_sync(kAll, sa, src + 4);
+      float b10 = __shfl_sync(kAll, sb, src), b11 = __shfl_sync(kAll, sb, src + 4);
+      uint32_t bhi0, blo0, bhi1, blo1;
+      split2(b00, b01, &bhi0, &blo0);
+      split2(b10, b11, &bhi1, &blo1);
+      const uint32_t B0 = gr >= 4 ? 0u : (gr & 1) ? blo0 : bhi0;
+      const uint32_t B1 = gr >= 4 ? 0u : (gr & 1) ? blo1 : bhi1;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        mma(acc[2 * c], transpose8x8(ka[c].x), transpose8x8(ka[c].y),
+            transpose8x8(kb[c].x), transpose8x8(kb[c].y), B0, B1);
+        mma(acc[2 * c + 1], transpose8x8(ka[c].z), transpose8x8(ka[c].w),
+            transpose8x8(kb[c].z), transpose8x8(kb[c].w), B0, B1);
+      }
+    }
+#pragma unroll
+    for (int off = 4; off <= 16; off <<= 1) {
+      l += __shfl_xor_sync(kAll, l, off);
+      E += __shfl_xor_sync(kAll, E, off);
+    }
+    l += l0;
+    E += E0;
+    const float inv = 1.f / l, Di = E * inv, lse = m + log2f(l);
+    if (lane == 0) {
+      s_m[rr] = lse;
+      s_E[rr] = Di;
+      a.stats[row] = make_float2(lse, Di);
+    }
+    // lanes tq = 0 hold A, tq = 1 Bk, of dimensions 32 c + 8 (gr / 2) +
+    // gr % 2 + {0, 2, 4, 6}
+#pragma unroll
+    for (int t = 0; t < 2 * NC; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float v = acc[t][2 * u] + acc[t][2 * u + 1];
+        const float o = __shfl_down_sync(kAll, v, 1);
+        if (tq == 0)
+          s_dq[rr * D + 32 * (t / 2) + 8 * (gr >> 1) + (gr & 1) + 4 * (t & 1) +
+               2 * u] = (v - Di * o) * inv * sc;
+      }
+    __syncwarp();
+    float2* pds = a.pds + row * (k + 1);
+    for (int t = lane; t < k; t += 32) {
+      float2 o = make_float2(0.f, 0.f);
+      if (t < mt) {
+        const float2 xd = s_xd[t];
+        o.x = exp2f(xd.x - lse);  // 0 where the slot was refused
+        o.y = o.x * (xd.y - Di) * sc;
+      }
+      pds[1 + t] = o;
+    }
+    __syncwarp();
+  }
+
+  // ---- 3: dS of the window and the anchor
+  {
+    uint32_t qa[KS][4], ga[NP][KS][4];
+    fragments(qa, ga);
+    float o[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[t][c] = 0.f;
+    const float lse[2] = {s_m[gr], s_m[gr + 8]}, Di[2] = {s_E[gr], s_E[gr + 8]};
+#pragma unroll 1
+    for (int ch = m0; ch < nch; ++ch) {
+      stage(ch);
+      __syncthreads();
+      const int cs = ch < 0 ? 0 : cs0 + ch * CK;
+      const int jlo = ch < 0 ? 0 : max(cs, kmin & ~15);
+      const int jhi = ch < 0 ? (anchors ? 0 : -1) : min(cs + CK - 1, kmax);
+#pragma unroll 1
+      for (int kb = jlo; wlive && kb <= jhi; kb += 16) {
+        float x[2][4], dp[2][4];
+        block(qa, ga, kb, kb - cs, ch < 0, x, dp);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float p = exp2f(x[t][c] - lse[c >> 1]);
+            const float ds = p * (dp[t][c] - Di[c >> 1]) * sc;
+            if (ch < 0 && t == 0 && (c & 1) == 0 && tq == 0 &&
+                (c ? vb : va))  // the anchor's entry (zeros without one)
+              a.pds[(rowbase + (c ? rb : ra)) * (k + 1)] = make_float2(p, ds);
+            x[t][c] = ds;
+          }
+        uint32_t hi[4], lo[4];
+        split2(x[0][0], x[0][1], &hi[0], &lo[0]);
+        split2(x[0][2], x[0][3], &hi[1], &lo[1]);
+        split2(x[1][0], x[1][1], &hi[2], &lo[2]);
+        split2(x[1][2], x[1][3], &hi[3], &lo[3]);
+        const unsigned char* kr = sK + (kb - cs + (lane & 15)) * RS +
+                                  (lane >> 4) * 16;
+#pragma unroll
+        for (int t = 0; t < NT; t += 2) {
+          uint32_t f[4];
+          ldsm4t(f, kr + t * 16);
+          mma(o[t], hi[0], hi[1], hi[2], hi[3], f[0], f[1]);
+          mma(o[t], lo[0], lo[1], lo[2], lo[3], f[0], f[1]);
+          mma(o[t + 1], hi[0], hi[1], hi[2], hi[3], f[2], f[3]);
+          mma(o[t + 1], lo[0], lo[1], lo[2], lo[3], f[2], f[3]);
+        }
+      }
+      __syncthreads();
+    }
+    if (!wlive) return;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float* pa = s_dq + gr * D + 8 * t + 2 * tq;
+      float* pb = pa + 8 * D;
+      pa[0] += o[t][0];
+      pa[1] += o[t][1];
+      pb[0] += o[t][2];
+      pb[1] += o[t][3];
+    }
+    __syncwarp();
+    constexpr int kPieces = D / 8;
+    bf* dQ = reinterpret_cast<bf*>(a.dQ) + (rowbase + i0) * D;
+    for (int e = lane; e < 16 * kPieces; e += 32)
+      if (i0 + e / kPieces < nq)
+        reinterpret_cast<uint4*>(dQ)[e] = pack16<bf>(s_dq + e * 8);
+  }
+}
+
+// ------------------------------------------------------------- listed pass
+// A warp sums kRange consecutive sorted entries, 16 at a time: their q (and
+// dO) rows, one row per four lanes, are transposed in registers into the A
+// operand (dimensions x entries); the B operand has two columns (hi, lo) for
+// each of four consecutive keys, an entry's weight standing in its key's
+// columns.  So a key's sums lie in the lanes of one column pair, whatever
+// the lengths of the keys' lists, and four keys are written at once.
+constexpr int kListedWarps = 4;
+
+template <int D, int NP>
+__global__ void __launch_bounds__(kListedWarps * 32)
+backward_listed_mma(Args a, const uint32_t* keys, const uint32_t* ents) {
+  constexpr int NC = D / 32;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int gr = lane >> 2, tq = lane & 3;
+  const int seg = blockIdx.y;
+  const int range = blockIdx.x * kListedWarps + wid;
+  if (range >= a.w.ranges) return;  // no barrier in this kernel
+  constexpr int NU = kRange / 32;
+  const int64_t base = (int64_t)seg * a.w.per_head;
+  const int64_t x0 = (int64_t)range * kRange;
+  const int nx = (int)min((int64_t)kRange, a.w.per_head - x0);
+  const uint32_t L = (uint32_t)a.L;
+  const int64_t row0 = (int64_t)seg * (a.Hq / a.Hkv) * a.nq;
+  const bf* Q = reinterpret_cast<const bf*>(a.Q) + row0 * D + 8 * tq;
+  const bf* G[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) G[p] = a.g[p] + row0 * D + 8 * tq;
+
+  // the range's keys, rows and weights (each weight as hi | lo << 16), entry
+  // 32 u + lane; where keys begin and end
+  uint32_t key[NU], row[NU], wp[NU], wd[NU], heads[NU];
+  int n = 0;  // entries in use
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    const int x = 32 * u + lane;
+    key[u] = x < nx ? keys[base + x0 + x] : L;
+    row[u] = x < nx ? ents[base + x0 + x] : 0u;
+  }
+  const uint32_t before = x0 > 0 ? keys[base + x0 - 1] : 0xFFFFFFFFu;
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    const bool use = key[u] < L;
+    const float2 pd = use ? a.pds[base + row[u]] : make_float2(0.f, 0.f);
+    row[u] /= (uint32_t)(a.k + 1);
+    const float ph = __bfloat162float(__float2bfloat16_rn(pd.x));
+    const float dh = __bfloat162float(__float2bfloat16_rn(pd.y));
+    wp[u] = pack2(ph, pd.x - ph);
+    wd[u] = pack2(dh, pd.y - dh);
+    uint32_t prev = __shfl_up_sync(kAll, key[u], 1);
+    const uint32_t last = u ? __shfl_sync(kAll, key[u ? u - 1 : 0], 31) : before;
+    if (lane == 0) prev = last;
+    const bool head = key[u] != prev;
+    heads[u] = __ballot_sync(kAll, head && use);
+    n += __popc(__ballot_sync(kAll, use));
+    const int x = 32 * u + lane;
+    if (head && x < nx) {
+      if (use) a.span[(int64_t)seg * L + key[u]].x = (int)(x0 + x);
+      if (x0 + x > 0 && prev < L) a.span[(int64_t)seg * L + prev].y = (int)(x0 + x);
+    }
+    if (use && x0 + x + 1 == a.w.per_head)
+      a.span[(int64_t)seg * L + key[u]].y = (int)(x0 + x + 1);
+  }
+  if (n == 0) return;
+
+  float dk[2 * NC][4], dv[2 * NC][4];
+  auto clear = [&]() {
+#pragma unroll
+    for (int t = 0; t < 2 * NC; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) dk[t][c] = dv[t][c] = 0.f;
+  };
+  clear();
+  uint32_t mykey = L;  // key of this lane's column pair; L: none
+  bool carried = (heads[0] & 1u) == 0;  // pair 0 began in an earlier range
+  int cur = -1;  // column pair of the last entry so far
+  if (carried) {
+    cur = 0;
+    if (tq == 0) mykey = before;
+  }
+  auto flush = [&]() {
+    if (mykey < L) {
+      float* o = carried && tq == 0
+          ? a.carry + ((int64_t)seg * a.w.ranges + range) * 2 * D
+          : a.top + ((int64_t)seg * L + mykey) * 2 * D;
+      o += 8 * (gr >> 1) + (gr & 1);
+#pragma unroll
+      for (int t = 0; t < 2 * NC; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int at = 32 * (t / 2) + 4 * (t & 1) + 2 * u;
+          o[at] = dk[t][2 * u] + dk[t][2 * u + 1];
+          o[D + at] = dv[t][2 * u] + dv[t][2 * u + 1];
+        }
+    }
+    mykey = L;
+    carried = false;
+  };
+
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+#pragma unroll 1
+    for (int hf = 0; hf < 2; ++hf) {
+      const int g0 = 32 * u + 16 * hf;
+      if (g0 >= n) break;
+      const int cnt = min(16, n - g0);
+      // the rows of entries gr and gr + 8
+      const int ea = 16 * hf + gr;
+      const uint32_t rra = __shfl_sync(kAll, row[u], ea);
+      const uint32_t rrb = __shfl_sync(kAll, row[u], ea + 8);
+      const bool la = gr < cnt, lb = gr + 8 < cnt;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      uint4 qa[NC], qb[NC], ga[NP][NC], gb[NP][NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int64_t pa = (int64_t)rra * D + 32 * c;
+        const int64_t pb = (int64_t)rrb * D + 32 * c;
+        qa[c] = la ? __ldg(reinterpret_cast<const uint4*>(Q + pa)) : zero;
+        qb[c] = lb ? __ldg(reinterpret_cast<const uint4*>(Q + pb)) : zero;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          ga[p][c] = la ? __ldg(reinterpret_cast<const uint4*>(G[p] + pa)) : zero;
+          gb[p][c] = lb ? __ldg(reinterpret_cast<const uint4*>(G[p] + pb)) : zero;
+        }
+      }
+      // weights of entries 2 tq, 2 tq + 1 and those + 8 (part gr & 1)
+      const int eb = 16 * hf + 2 * tq;
+      const int sh = (gr & 1) * 16;
+      uint32_t d0 = __shfl_sync(kAll, wd[u], eb) >> sh;
+      uint32_t d1 = __shfl_sync(kAll, wd[u], eb + 1) >> sh;
+      uint32_t d2 = __shfl_sync(kAll, wd[u], eb + 8) >> sh;
+      uint32_t d3 = __shfl_sync(kAll, wd[u], eb + 9) >> sh;
+      uint32_t p0 = __shfl_sync(kAll, wp[u], eb) >> sh;
+      uint32_t p1 = __shfl_sync(kAll, wp[u], eb + 1) >> sh;
+      uint32_t p2 = __shfl_sync(kAll, wp[u], eb + 8) >> sh;
+      uint32_t p3 = __shfl_sync(kAll, wp[u], eb + 9) >> sh;
+      const uint32_t hd = (heads[u] >> (16 * hf)) & 0xFFFFu;
+      uint32_t left = (1u << cnt) - 1u;  // entries still to be added
+      // usually once; again for each four keys when lists are short
+#pragma unroll 1
+      while (left) {
+        // place of each entry's key: cur + heads up to it among `left`
+        const uint32_t hl = hd & left;
+        const int me = lane & 15;
+        const int slot = cur + __popc(hl & ((2u << me) - 1u));
+        const bool act = lane < 16 && ((left >> me) & 1u) && slot < 4;
+        const uint32_t all = __ballot_sync(kAll, act);
+        uint32_t mt = 0, mn = 0;  // entries of this lane's pair, column
+        int top = cur;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t bm = __ballot_sync(kAll, act && slot == q);
+          if (q == tq) mt = bm;
+          if (q == (gr >> 1)) mn = bm;
+          if (bm) top = q;
+        }
+        const uint32_t kq =
+            __shfl_sync(kAll, key[u], 16 * hf + (mt ? __ffs(mt) - 1 : 0));
+        if (mt) mykey = kq;
+        cur = top;
+        const int e0 = 2 * tq;
+        const uint32_t z0 = ((mn >> e0) & 1u) ? 0xFFFFu : 0u;
+        const uint32_t z1 = ((mn >> (e0 + 1)) & 1u) ? 0xFFFFu : 0u;
+        const uint32_t z2 = ((mn >> (e0 + 8)) & 1u) ? 0xFFFFu : 0u;
+        const uint32_t z3 = ((mn >> (e0 + 9)) & 1u) ? 0xFFFFu : 0u;
+        const uint32_t D0 = (d0 & z0) | ((d1 & z1) << 16);
+        const uint32_t D1 = (d2 & z2) | ((d3 & z3) << 16);
+        const uint32_t P0 = (p0 & z0) | ((p1 & z1) << 16);
+        const uint32_t P1 = (p2 & z2) | ((p3 & z3) << 16);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          mma(dk[2 * c], transpose8x8(qa[c].x), transpose8x8(qa[c].y),
+              transpose8x8(qb[c].x), transpose8x8(qb[c].y), D0, D1);
+          mma(dk[2 * c + 1], transpose8x8(qa[c].z), transpose8x8(qa[c].w),
+              transpose8x8(qb[c].z), transpose8x8(qb[c].w), D0, D1);
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            mma(dv[2 * c], transpose8x8(ga[p][c].x), transpose8x8(ga[p][c].y),
+                transpose8x8(gb[p][c].x), transpose8x8(gb[p][c].y), P0, P1);
+            mma(dv[2 * c + 1], transpose8x8(ga[p][c].z),
+                transpose8x8(ga[p][c].w), transpose8x8(gb[p][c].z),
+                transpose8x8(gb[p][c].w), P0, P1);
+          }
+        }
+        left &= ~all;
+        if (left) {  // four keys are full: write them, go on with the next
+          flush();
+          clear();
+          cur = -1;
+        }
+      }
+    }
+  }
+  flush();
+}
+
+// ------------------------------------------------------------- column pass
+// A CTA owns 64 keys of one kv head, a warp 16: S^T and dP^T of 16 keys x 16
+// rows at a time, then dV += P^T dO and dK += dS^T Q with P^T and dS^T in two
+// parts straight from their accumulators.  Query rows are staged 64 at a
+// time with their log-sum-exp, D and window start; the listed part is added
+// at the end.
+constexpr int kColWarps = 4;
+
+template <int D, int NP>
+struct ColSmem {
+  static constexpr int RS = D * 2 + 16;
+  static constexpr size_t tile = (size_t)64 * RS;
+  static constexpr size_t bytes = (3 + NP) * tile + 64 * 12;
+};
+
+template <int D, int NP>
+__global__ void __launch_bounds__(kColWarps * 32)
+backward_columns_mma(Args a, int ntile) {
+  using SM = ColSmem<D, NP>;
+  constexpr int RS = SM::RS;
+  constexpr int KS = D / 16, NT = D / 8;
+  extern __shared__ __align__(16) unsigned char g_smem[];
+  unsigned char* sK = g_smem;
+  unsigned char* sV = sK + SM::tile;
+  unsigned char* sQ = sV + SM::tile;
+  unsigned char* sG = sQ + SM::tile;  // NP planes
+  float* s_lse = reinterpret_cast<float*>(sG + NP * SM::tile);
+  float* s_D = s_lse + 64;
+  int* s_lo = reinterpret_cast<int*>(s_D + 64);
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int gr = lane >> 2, tq = lane & 3;
+  const int L = a.L, nq = a.nq, G = a.Hq / a.Hkv;
+  const int seg = blockIdx.x / ntile;
+  const int j0 = (blockIdx.x % ntile) * 64;
+  const int b = seg / a.Hkv, g = seg % a.Hkv;
+  const int kw = j0 + wid * 16;  // the warp's first key
+  const float sl2 = kLog2e / sqrtf((float)D), sc = 1.f / sqrtf((float)D);
+  constexpr int kPieces = D * 2 / 16;
+  auto stage = [&](unsigned char* dst, const bf* src, int first, int limit) {
+    for (int e = threadIdx.x; e < 64 * kPieces; e += kColWarps * 32) {
+      const int rr = e / kPieces, pc = e % kPieces;
+      cp_async16(dst + rr * RS + pc * 16,
+                 src + (int64_t)min(first + rr, limit - 1) * D + pc * 8);
+    }
+  };
+  stage(sK, reinterpret_cast<const bf*>(a.K) + (int64_t)seg * L * D, j0, L);
+  stage(sV, reinterpret_cast<const bf*>(a.V) + (int64_t)seg * L * D, j0, L);
+  float dk[NT][4], dv[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) dk[t][c] = dv[t][c] = 0.f;
+  const int jl = min(j0 + 63, L - 1);  // the CTA's last key
+  const int chunks = (nq + kRowChunk - 1) / kRowChunk;
+#pragma unroll 1
+  for (int hh = 0; hh < G; ++hh) {
+    const int h = g * G + hh;
+    int wm = a.W_i ? a.wmax[b] : (a.W_h ? a.W_h[h] : a.W);
+    wm = min(max(wm, 1), L);
+    // rows whose position i has i - wm + 1 <= jl and i >= j0
+    const int rmin = max(j0 - a.p0, 0);
+    const int rmax = (int)min((int64_t)jl + wm - 1 - a.p0, (int64_t)nq - 1);
+    const int64_t rowbase = ((int64_t)b * a.Hq + h) * nq;
+#pragma unroll 1
+    for (int rc = rmin / 64 * 64; rc <= rmax; rc += 64) {
+      if (a.W_i && a.lows[b * chunks + rc / 64] > jl) continue;
+      __syncthreads();  // the last chunk has been read
+      stage(sQ, reinterpret_cast<const bf*>(a.Q) + rowbase * D, rc, nq);
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        stage(sG + p * SM::tile, a.g[p] + rowbase * D, rc, nq);
+      if (threadIdx.x < 64) {
+        const int r = rc + threadIdx.x;
+        int w, lo = 0x7FFFFFFF;  // rows behind the last: no key
+        float2 st = make_float2(0.f, 0.f);
+        if (r < nq) {
+          lo = window_lo(a, b, h, r, false, &w);
+          st = a.stats[rowbase + r];
+        }
+        s_lo[threadIdx.x] = lo;
+        s_lse[threadIdx.x] = st.x;
+        s_D[threadIdx.x] = st.y;
+      }
+      cp_async_wait_all();
+      __syncthreads();
+#pragma unroll 1
+      for (int rb = 0; rb < 64; rb += 16) {
+        // does any of these 16 rows see any of the warp's 16 keys?
+        const int rl = rb + (lane & 15);
+        if (!__any_sync(kAll, a.p0 + rc + rl >= kw && s_lo[rl] <= kw + 15))
+          continue;
+        float x[2][4], dp[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[t][c] = dp[t][c] = 0.f;
+        const int ar = wid * 16 + (lane & 15), ac = (lane >> 4) * 16;
+        const int br = rb + (lane & 7) + ((lane >> 4) << 3);
+        const int bc = ((lane >> 3) & 1) * 16;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t A[4], B[4];
+          ldsm4(A, sK + ar * RS + ks * 32 + ac);
+          ldsm4(B, sQ + br * RS + ks * 32 + bc);
+          mma(x[0], A[0], A[1], A[2], A[3], B[0], B[1]);
+          mma(x[1], A[0], A[1], A[2], A[3], B[2], B[3]);
+          ldsm4(A, sV + ar * RS + ks * 32 + ac);
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            ldsm4(B, sG + p * SM::tile + br * RS + ks * 32 + bc);
+            mma(dp[0], A[0], A[1], A[2], A[3], B[0], B[1]);
+            mma(dp[1], A[0], A[1], A[2], A[3], B[2], B[3]);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int rl2 = rb + 8 * t + 2 * tq + (c & 1);
+            const int j = kw + gr + (c >= 2 ? 8 : 0);
+            const bool ok = j <= a.p0 + rc + rl2 && j >= s_lo[rl2];
+            const float p = ok ? exp2f(x[t][c] * sl2 - s_lse[rl2]) : 0.f;
+            x[t][c] = p;
+            dp[t][c] = p * (dp[t][c] - s_D[rl2]) * sc;
+          }
+        uint32_t ph[4], pl[4], dh[4], dl[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          split2(x[c >> 1][(c & 1) * 2], x[c >> 1][(c & 1) * 2 + 1], &ph[c],
+                 &pl[c]);
+          split2(dp[c >> 1][(c & 1) * 2], dp[c >> 1][(c & 1) * 2 + 1], &dh[c],
+                 &dl[c]);
+        }
+        const int tr = (rb + (lane & 15)) * RS + (lane >> 4) * 16;
+#pragma unroll
+        for (int t = 0; t < NT; t += 2) {
+          uint32_t f[4];
+          ldsm4t(f, sQ + tr + t * 16);
+          mma(dk[t], dh[0], dh[1], dh[2], dh[3], f[0], f[1]);
+          mma(dk[t], dl[0], dl[1], dl[2], dl[3], f[0], f[1]);
+          mma(dk[t + 1], dh[0], dh[1], dh[2], dh[3], f[2], f[3]);
+          mma(dk[t + 1], dl[0], dl[1], dl[2], dl[3], f[2], f[3]);
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            ldsm4t(f, sG + p * SM::tile + tr + t * 16);
+            mma(dv[t], ph[0], ph[1], ph[2], ph[3], f[0], f[1]);
+            mma(dv[t + 1], ph[0], ph[1], ph[2], ph[3], f[2], f[3]);
+            if (p == 0) {  // lo x lo is below what two parts keep
+              mma(dv[t], pl[0], pl[1], pl[2], pl[3], f[0], f[1]);
+              mma(dv[t + 1], pl[0], pl[1], pl[2], pl[3], f[2], f[3]);
+            }
+          }
+        }
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // K and V, if unused
+  // the listed part, then out
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int j = kw + gr + 8 * u;
+    if (j >= L) continue;
+    const int64_t col = (int64_t)seg * L + j;
+    const int2 sp = a.span[col];
+    if (sp.y > sp.x) {
+      const float* t0 = a.top + col * 2 * D + 2 * tq;
+      const int r1 = (sp.y - 1) / kRange;
+      for (int r = sp.x / kRange; r <= r1; ++r) {
+        const float* p = r == sp.x / kRange
+            ? t0
+            : a.carry + ((int64_t)seg * a.w.ranges + r) * 2 * D + 2 * tq;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float2 k2 = *reinterpret_cast<const float2*>(p + 8 * t);
+          const float2 v2 = *reinterpret_cast<const float2*>(p + D + 8 * t);
+          dk[t][2 * u] += k2.x;
+          dk[t][2 * u + 1] += k2.y;
+          dv[t][2 * u] += v2.x;
+          dv[t][2 * u + 1] += v2.y;
+        }
+      }
+    }
+    uint32_t* ok = reinterpret_cast<uint32_t*>(
+        reinterpret_cast<bf*>(a.dK) + col * D + 2 * tq);
+    uint32_t* ov = reinterpret_cast<uint32_t*>(
+        reinterpret_cast<bf*>(a.dV) + col * D + 2 * tq);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      ok[4 * t] = pack2(dk[t][2 * u], dk[t][2 * u + 1]);
+      ov[4 * t] = pack2(dv[t][2 * u], dv[t][2 * u + 1]);
+    }
+  }
+}
+
+// --------------------------------------------------------------- host side
+template <int D, int NP>
+cudaError_t rows_as(const Args& a, cudaStream_t s) {
+  const int ntile = (a.nq + 63) / 64;
+  const int64_t ctas = (int64_t)a.B * a.Hq * ntile;
+  if (ctas > 0x7FFFFFFF) return cudaErrorNotSupported;
+  const size_t smem = RowSmem<D>::bytes(a.k);
+  auto kern = backward_rows_mma<D, NP>;
+  cudaError_t e = ensure_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  prof_before(s, "backward_rows");
+  kern<<<(unsigned)ctas, kRowWarps * 32, smem, s>>>(a, ntile);
+  prof_after(s);
+  return cudaGetLastError();
+}
+
+template <int D, int NP>
+cudaError_t listed_as(const Args& a, const uint32_t* keys,
+                      const uint32_t* ents, cudaStream_t s) {
+  prof_before(s, "backward_listed");
+  backward_listed_mma<D, NP>
+      <<<dim3((a.w.ranges + kListedWarps - 1) / kListedWarps, a.w.segs),
+         kListedWarps * 32, 0, s>>>(a, keys, ents);
+  prof_after(s);
+  return cudaGetLastError();
+}
+
+template <int D, int NP>
+cudaError_t columns_as(const Args& a, cudaStream_t s) {
+  const int ntile = (a.L + 63) / 64;
+  const int64_t ctas = (int64_t)a.w.segs * ntile;
+  if (ctas > 0x7FFFFFFF) return cudaErrorNotSupported;
+  auto kern = backward_columns_mma<D, NP>;
+  cudaError_t e = ensure_smem(kern, ColSmem<D, NP>::bytes);
+  if (e != cudaSuccess) return e;
+  prof_before(s, "backward_columns");
+  kern<<<(unsigned)ctas, kColWarps * 32, ColSmem<D, NP>::bytes, s>>>(a, ntile);
+  prof_after(s);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t rows_mma_launch(const Args& a, int d, cudaStream_t s) {
+  if (d == 64) return a.g[1] ? rows_as<64, 2>(a, s) : rows_as<64, 1>(a, s);
+  return a.g[1] ? rows_as<128, 2>(a, s) : rows_as<128, 1>(a, s);
+}
+
+cudaError_t listed_mma_launch(const Args& a, int d, const uint32_t* keys,
+                              const uint32_t* ents, cudaStream_t s) {
+  if (d == 64)
+    return a.g[1] ? listed_as<64, 2>(a, keys, ents, s)
+                  : listed_as<64, 1>(a, keys, ents, s);
+  return a.g[1] ? listed_as<128, 2>(a, keys, ents, s)
+                : listed_as<128, 1>(a, keys, ents, s);
+}
+
+cudaError_t columns_mma_launch(const Args& a, int d, cudaStream_t s) {
+  if (d == 64)
+    return a.g[1] ? columns_as<64, 2>(a, s) : columns_as<64, 1>(a, s);
+  return a.g[1] ? columns_as<128, 2>(a, s) : columns_as<128, 1>(a, s);
+}
+
+}  // namespace bwd
+}  // namespace ca

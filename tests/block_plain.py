@@ -104,8 +104,10 @@ def attention_backward(Q, K, V, dO, idx):
     the exponentials, the running maximum's rescales and the sum; dP by
     (d + 4) 2 U sum|dO v|; D by the sum of its terms' errors.  dS is taken as
     e dP - D e, so its terms count with |dP| + |D|.  bf16 operands of a
-    matrix product hold p and dS in two parts (2^-16 relative).  The sums
-    over rows or keys add (their length + 8) 2 U of their magnitudes."""
+    matrix product hold p and dS in two parts (2^-16 relative), and an fp32 dO
+    beside bf16 inputs as well (2^-16 in dP; in dV its lo part meets p's hi
+    part only, 2^-16 more).  The sums over rows or keys add (their length + 8)
+    2 U of their magnitudes."""
     d, L = Q.shape[-1], K.shape[2]
     B, Hkv = K.shape[:2]
     G = Q.shape[1] // Hkv
@@ -123,8 +125,9 @@ def attention_backward(Q, K, V, dO, idx):
     dS = P * (dP - D) * sc
     C = idx.shape[-1]
     split = 2.0 ** -16 if Q.dtype == torch.bfloat16 else 0.0
+    planes = split if dO.dtype == torch.float32 else 0.0
     rp = 2 * eS + (4 * C + 64) * U + split
-    edP = 2 * (d + 4) * U * (Gd.abs() @ T(Vd.abs()))
+    edP = (2 * (d + 4) * U + planes) * (Gd.abs() @ T(Vd.abs()))
     eD = (P * (edP + rp * dP.abs())).sum(-1, keepdim=True)
     edS = sc * P * (rp * (dP.abs() + D.abs()) + edP + eD)
     mag = sc * P * (dP.abs() + D.abs())
@@ -134,7 +137,7 @@ def attention_backward(Q, K, V, dO, idx):
     n = m.sum(-2).unflatten(1, (Hkv, G)).sum(2)[..., None]  # rows of a key
     dK, dV = group(T(dS) @ Qd), group(T(P) @ Gd)
     bK = group(T(edS) @ Qd.abs()) + 2 * (n + 8) * U * group(T(mag) @ Qd.abs())
-    bV = group(T(rp * P) @ Gd.abs()) + 2 * (n + 8) * U * \
+    bV = group(T((rp + 2 * planes) * P) @ Gd.abs()) + 2 * (n + 8) * U * \
         group(T(P) @ Gd.abs())
     return (dQ, bQ), (dK, bK), (dV, bV)
 
