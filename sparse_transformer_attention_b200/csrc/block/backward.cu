@@ -257,73 +257,129 @@ __global__ void __launch_bounds__(kRowWarps * 32) backward_rows(Args a) {
 }
 
 // ------------------------------------------------- listed part of dK and dV
-// A warp sums kRange consecutive sorted entries, one key after the other, so
-// that the work is even however many rows list a key.  A key's sum goes to
-// `top` if it began in this range, else (the range's head) to `carry`.
+// kRange consecutive sorted entries are summed by the lanes that hold one
+// row, 16 bytes each (8 to 32 lanes; a warp works on one to four ranges side
+// by side), key after key, so that the work is even however many rows list a
+// key.  A key's sum goes to `top` if it began in this range, else (the
+// range's head) to `carry`.
+//
+// Bound by what reaches a row's registers: 256 bytes of q and dO per entry
+// (bf16, d = 64), read anywhere in the head's rows.  With eight neighbouring
+// lanes on one 128-byte row a load is four wavefronts of the L1 data pipe;
+// matrix-instruction layouts, which need rows spread over lanes in steps of
+// four, take 8 to 16 and left that pipe full (92% of its cycles) at 290 us in
+// the 8K GPT-2-small case.  Plain fp32 FMA keep the weights whole, too.
+constexpr int kListedWarps = 4;
+
 template <typename T, typename TD, int D>
-__global__ void __launch_bounds__(256) backward_listed(Args a,
-                                                       const uint32_t* keys,
-                                                       const uint32_t* ents) {
-  constexpr int DL = D / 32;
+__global__ void __launch_bounds__(kListedWarps * 32)
+backward_listed(Args a, const uint32_t* keys, const uint32_t* ents) {
+  constexpr int EPL = Elem<T>::kPer16B;  // elements per lane
+  constexpr int LPR = D / EPL;           // lanes per row
+  constexpr int SUBS = 32 / LPR;         // ranges per warp
+  constexpr int U = 4;                   // entries read at a time
+  __shared__ uint4 s_ent[kListedWarps][SUBS * kRange];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int sub = lane / LPR, sl = lane % LPR;
   const int seg = blockIdx.y;
-  const int range = blockIdx.x * 8 + wid;
-  if (range >= a.w.ranges) return;
+  const int64_t first = ((int64_t)blockIdx.x * kListedWarps + wid) * SUBS;
+  if (first >= a.w.ranges) return;  // no barrier of the CTA in this kernel
   const int64_t base = (int64_t)seg * a.w.per_head;
-  const int64_t x0 = (int64_t)range * kRange;
-  const int64_t x1 = min(x0 + kRange, a.w.per_head);
-  const T* Q = reinterpret_cast<const T*>(a.Q) + lane * DL;
-  const TD* dO = reinterpret_cast<const TD*>(a.dO) + lane * DL;
-  const int64_t row0 = (int64_t)seg * (a.Hq / a.Hkv) * a.nq;
-  const float2* pds = a.pds + base;
+  const int64_t w0 = first * kRange;  // the warp's first entry
   const uint32_t L = (uint32_t)a.L;
-  uint32_t cur = x0 > 0 ? keys[base + x0 - 1] : 0xFFFFFFFFu;
-  bool head = x0 > 0;  // the sum so far belongs to a key begun earlier
-  float dk[DL], dv[DL];
+  // the warp's entries: key, row, p, dS; where keys begin and end
+  uint4* ent = s_ent[wid];
+  {
+    constexpr int NU = SUBS * kRange / 32;
+    uint32_t key[NU], e[NU];
+    float2 pd[NU];
 #pragma unroll
-  for (int c = 0; c < DL; ++c) dk[c] = dv[c] = 0.f;
+    for (int u = 0; u < NU; ++u) {
+      const int64_t x = w0 + 32 * u + lane;
+      key[u] = x < a.w.per_head ? keys[base + x] : L;
+      e[u] = x < a.w.per_head ? ents[base + x] : 0u;
+    }
+    uint32_t before = w0 > 0 ? keys[base + w0 - 1] : 0xFFFFFFFFu;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+      pd[u] = key[u] < L ? a.pds[base + e[u]] : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const bool use = key[u] < L;
+      ent[32 * u + lane] = make_uint4(
+          key[u], use ? e[u] / (uint32_t)(a.k + 1) : 0u,
+          __float_as_uint(pd[u].x), __float_as_uint(pd[u].y));
+      uint32_t prev = __shfl_up_sync(kAll, key[u], 1);
+      if (lane == 0) prev = before;
+      before = __shfl_sync(kAll, key[u], 31);
+      const int64_t x = w0 + 32 * u + lane;
+      if (key[u] != prev && x < a.w.per_head) {
+        if (use) a.span[(int64_t)seg * L + key[u]].x = (int)x;
+        if (x > 0 && prev < L) a.span[(int64_t)seg * L + prev].y = (int)x;
+      }
+      if (use && x + 1 == a.w.per_head)
+        a.span[(int64_t)seg * L + key[u]].y = (int)(x + 1);
+    }
+    if (__all_sync(kAll, key[0] >= L)) return;  // sorted: none in use
+  }
+  const int64_t range = first + sub;
+  uint32_t cur = range * kRange > 0 && range < a.w.ranges
+                     ? (sub ? ent[sub * kRange - 1].x : keys[base + w0 - 1])
+                     : 0xFFFFFFFFu;
+  __syncwarp();
+  ent += sub * kRange;
+  const int64_t at0 =
+      (int64_t)seg * (a.Hq / a.Hkv) * a.nq * D + sl * EPL;
+  const T* Q = reinterpret_cast<const T*>(a.Q) + at0;
+  const TD* G = reinterpret_cast<const TD*>(a.dO) + at0;
+  bool head = cur < L;  // the sum so far belongs to a key begun earlier
+  float dk[EPL], dv[EPL];
+#pragma unroll
+  for (int c = 0; c < EPL; ++c) dk[c] = dv[c] = 0.f;
   auto flush = [&]() {
-    float* o = nullptr;
-    if (head)
-      o = a.carry + ((int64_t)seg * a.w.ranges + range) * 2 * D;
-    else if (cur < L)
-      o = a.top + ((int64_t)seg * L + cur) * 2 * D;
-    if (!o) return;
+    if (cur >= L) return;
+    float* o = (head ? a.carry + ((int64_t)seg * a.w.ranges + range) * 2 * D
+                     : a.top + ((int64_t)seg * L + cur) * 2 * D) +
+               sl * EPL;
 #pragma unroll
-    for (int c = 0; c < DL; ++c) {
-      o[lane * DL + c] = dk[c];
-      o[D + lane * DL + c] = dv[c];
+    for (int c = 0; c < EPL; c += 4) {
+      *reinterpret_cast<float4*>(o + c) =
+          make_float4(dk[c], dk[c + 1], dk[c + 2], dk[c + 3]);
+      *reinterpret_cast<float4*>(o + D + c) =
+          make_float4(dv[c], dv[c + 1], dv[c + 2], dv[c + 3]);
     }
   };
-  for (int64_t x = x0; x < x1; ++x) {
-    const uint32_t kj = keys[base + x];
-    if (kj != cur) {
-      if (x > x0 || head) flush();
-      head = false;
-      if (lane == 0) {
-        if (x > 0 && cur < L) a.span[(int64_t)seg * L + cur].y = (int)x;
-        if (kj < L) a.span[(int64_t)seg * L + kj].x = (int)x;
-      }
-      cur = kj;
+#pragma unroll 1
+  for (int x = 0; x < kRange; x += U) {
+    uint4 en[U];
+    uint4 q[U];
+    float g[U][EPL];
 #pragma unroll
-      for (int c = 0; c < DL; ++c) dk[c] = dv[c] = 0.f;
+    for (int u = 0; u < U; ++u) {
+      en[u] = ent[x + u];
+      q[u] = __ldg(reinterpret_cast<const uint4*>(Q + (int64_t)en[u].y * D));
+      load_row<TD, EPL>(G + (int64_t)en[u].y * D, g[u]);
     }
-    if (kj >= L) break;  // unused slots: nothing follows
-    const uint32_t e = ents[base + x];
-    const float2 pd = pds[e];
-    const int64_t row = row0 + e / (uint32_t)(a.k + 1);
-    float q[DL], g[DL];
-    load_f32<T, DL>(Q + row * D, q);
-    load_f32<TD, DL>(dO + row * D, g);
 #pragma unroll
-    for (int c = 0; c < DL; ++c) {
-      dk[c] = fmaf(pd.y, q[c], dk[c]);
-      dv[c] = fmaf(pd.x, g[c], dv[c]);
+    for (int u = 0; u < U; ++u) {
+      if (en[u].x != cur) {
+        flush();
+        head = false;
+        cur = en[u].x;
+#pragma unroll
+        for (int c = 0; c < EPL; ++c) dk[c] = dv[c] = 0.f;
+      }
+      const float p = __uint_as_float(en[u].z), ds = __uint_as_float(en[u].w);
+      float f[EPL];
+      Elem<T>::unpack(q[u], f);
+#pragma unroll
+      for (int c = 0; c < EPL; ++c) {
+        dk[c] = fmaf(ds, f[c], dk[c]);
+        dv[c] = fmaf(p, g[u][c], dv[c]);
+      }
     }
   }
-  if (cur < L || head) flush();
-  if (x1 == a.w.per_head && cur < L && lane == 0)
-    a.span[(int64_t)seg * L + cur].y = (int)x1;
+  flush();
 }
 
 // ------------------------------------------------------------- column pass
@@ -380,6 +436,24 @@ __global__ void __launch_bounds__(256) backward_columns(Args a) {
       }
     }
   }
+  // the listed part: what began in the key's first range, then the later
+  // ranges' shares, four at a time
+  const int2 sp = a.span[col];
+  if (sp.y > sp.x) {
+    const int r0 = sp.x / kRange, r1 = (sp.y - 1) / kRange;
+#pragma unroll 4
+    for (int r = r0 + grp; r <= r1; r += 4) {
+      const float* t =
+          (r == r0 ? a.top + col * 2 * D
+                   : a.carry + ((int64_t)seg * a.w.ranges + r) * 2 * D) +
+          sub * DL;
+#pragma unroll
+      for (int c = 0; c < DL; ++c) {
+        dk[c] += t[c];
+        dv[c] += t[D + c];
+      }
+    }
+  }
 #pragma unroll
   for (int off = 8; off <= 16; off <<= 1)
 #pragma unroll
@@ -388,23 +462,6 @@ __global__ void __launch_bounds__(256) backward_columns(Args a) {
       dv[c] += __shfl_xor_sync(kAll, dv[c], off);
     }
   if (grp != 0) return;
-  const int2 sp = a.span[col];
-  if (sp.y > sp.x) {
-    const float* t = a.top + col * 2 * D + sub * DL;
-#pragma unroll
-    for (int c = 0; c < DL; ++c) {
-      dk[c] += t[c];
-      dv[c] += t[D + c];
-    }
-    for (int r = sp.x / kRange + 1; r <= (sp.y - 1) / kRange; ++r) {
-      const float* cr = a.carry + ((int64_t)seg * a.w.ranges + r) * 2 * D + sub * DL;
-#pragma unroll
-      for (int c = 0; c < DL; ++c) {
-        dk[c] += cr[c];
-        dv[c] += cr[D + c];
-      }
-    }
-  }
   store_row<T, DL>(reinterpret_cast<T*>(a.dK) + col * D + sub * DL, dk);
   store_row<T, DL>(reinterpret_cast<T*>(a.dV) + col * D + sub * DL, dv);
 }
@@ -451,13 +508,14 @@ cudaError_t launch_as(Args a, cudaStream_t s) {
   e = cudaMemsetAsync(a.span, 0, (size_t)w.segs * a.L * 8, s);
   if (e != cudaSuccess) return e;
   const uint32_t *keys = a.key[last], *ents = a.ent[last];
+  constexpr int kPer = kListedWarps * 32 * Elem<T>::kPer16B / D;  // ranges
+  e = run("backward_listed", backward_listed<T, TD, D>,
+          dim3((w.ranges + kPer - 1) / kPer, w.segs), kListedWarps * 32, 0, s,
+          a, keys, ents);
+  if (e != cudaSuccess) return e;
   if constexpr (kMma) {
-    if ((e = listed_mma_launch(a, D, keys, ents, s)) != cudaSuccess) return e;
     return columns_mma_launch(a, D, s);
   } else {
-    e = run("backward_listed", backward_listed<T, TD, D>,
-            dim3((w.ranges + 7) / 8, w.segs), 256, 0, s, a, keys, ents);
-    if (e != cudaSuccess) return e;
     return run("backward_columns", backward_columns<T, TD, D>,
                dim3((unsigned)(((int64_t)w.segs * a.L + 7) / 8)), 256, 0, s,
                a);
@@ -499,7 +557,11 @@ cudaError_t backward_launch(const BackwardArgs& in, bool bf16, int d, void* ws,
   if (e != cudaSuccess) return e;
   using bf = __nv_bfloat16;
   if (bf16) {
-    return d == 64 ? launch_as<bf, bf, 64>(a, s) : launch_as<bf, bf, 128>(a, s);
+    if (a.do_bf16)
+      return d == 64 ? launch_as<bf, bf, 64>(a, s)
+                     : launch_as<bf, bf, 128>(a, s);
+    return d == 64 ? launch_as<bf, float, 64>(a, s)
+                   : launch_as<bf, float, 128>(a, s);
   }
   if (a.do_bf16)
     return d == 64 ? launch_as<float, bf, 64>(a, s)

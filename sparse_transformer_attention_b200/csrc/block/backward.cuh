@@ -15,7 +15,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // anchor (when it lies outside the window), slots 1..k the Top-k positions
 // in the order of idx; unused slots hold key L, which sorts behind all keys.
 constexpr int kTile = 4096;   // entries per CTA of the sort
-constexpr int kRange = 128;   // sorted entries per warp of the listed pass
+constexpr int kRange = 64;    // sorted entries of a sum of the listed pass
 constexpr int kRowChunk = 64; // query rows staged at a time by the columns
 
 struct Work {
@@ -76,10 +76,8 @@ __device__ __forceinline__ int listed_count(const Args& a, int64_t row, int i,
 // keys in entry order, starting from a.key[0] (entry numbers implied).  The
 // result is in a.key[*last], a.ent[*last].
 cudaError_t sort_launch(const Args& a, int* last, cudaStream_t s);
-// The row pass, the listed pass and the column pass on tensor cores (bf16).
+// The row pass and the column pass on matrix instructions (bf16).
 cudaError_t rows_mma_launch(const Args& a, int d, cudaStream_t s);
-cudaError_t listed_mma_launch(const Args& a, int d, const uint32_t* keys,
-                              const uint32_t* ents, cudaStream_t s);
 cudaError_t columns_mma_launch(const Args& a, int d, cudaStream_t s);
 
 }  // namespace bwd

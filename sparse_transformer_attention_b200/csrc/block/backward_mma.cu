@@ -99,7 +99,7 @@ struct RowSmem {
 };
 
 template <int D, int NP>
-__global__ void __launch_bounds__(kRowWarps * 32)
+__global__ void __launch_bounds__(kRowWarps * 32, D == 64 ? 4 : 2)
 backward_rows_mma(Args a, int ntile) {
   using SM = RowSmem<D>;
   constexpr int RS = SM::RS, CK = SM::CK;
@@ -528,202 +528,6 @@ backward_rows_mma(Args a, int ntile) {
   }
 }
 
-// ------------------------------------------------------------- listed pass
-// A warp sums kRange consecutive sorted entries, 16 at a time: their q (and
-// dO) rows, one row per four lanes, are transposed in registers into the A
-// operand (dimensions x entries); the B operand has two columns (hi, lo) for
-// each of four consecutive keys, an entry's weight standing in its key's
-// columns.  So a key's sums lie in the lanes of one column pair, whatever
-// the lengths of the keys' lists, and four keys are written at once.
-constexpr int kListedWarps = 4;
-
-template <int D, int NP>
-__global__ void __launch_bounds__(kListedWarps * 32)
-backward_listed_mma(Args a, const uint32_t* keys, const uint32_t* ents) {
-  constexpr int NC = D / 32;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int gr = lane >> 2, tq = lane & 3;
-  const int seg = blockIdx.y;
-  const int range = blockIdx.x * kListedWarps + wid;
-  if (range >= a.w.ranges) return;  // no barrier in this kernel
-  constexpr int NU = kRange / 32;
-  const int64_t base = (int64_t)seg * a.w.per_head;
-  const int64_t x0 = (int64_t)range * kRange;
-  const int nx = (int)min((int64_t)kRange, a.w.per_head - x0);
-  const uint32_t L = (uint32_t)a.L;
-  const int64_t row0 = (int64_t)seg * (a.Hq / a.Hkv) * a.nq;
-  const bf* Q = reinterpret_cast<const bf*>(a.Q) + row0 * D + 8 * tq;
-  const bf* G[NP];
-#pragma unroll
-  for (int p = 0; p < NP; ++p) G[p] = a.g[p] + row0 * D + 8 * tq;
-
-  // the range's keys, rows and weights (each weight as hi | lo << 16), entry
-  // 32 u + lane; where keys begin and end
-  uint32_t key[NU], row[NU], wp[NU], wd[NU], heads[NU];
-  int n = 0;  // entries in use
-#pragma unroll
-  for (int u = 0; u < NU; ++u) {
-    const int x = 32 * u + lane;
-    key[u] = x < nx ? keys[base + x0 + x] : L;
-    row[u] = x < nx ? ents[base + x0 + x] : 0u;
-  }
-  const uint32_t before = x0 > 0 ? keys[base + x0 - 1] : 0xFFFFFFFFu;
-#pragma unroll
-  for (int u = 0; u < NU; ++u) {
-    const bool use = key[u] < L;
-    const float2 pd = use ? a.pds[base + row[u]] : make_float2(0.f, 0.f);
-    row[u] /= (uint32_t)(a.k + 1);
-    const float ph = __bfloat162float(__float2bfloat16_rn(pd.x));
-    const float dh = __bfloat162float(__float2bfloat16_rn(pd.y));
-    wp[u] = pack2(ph, pd.x - ph);
-    wd[u] = pack2(dh, pd.y - dh);
-    uint32_t prev = __shfl_up_sync(kAll, key[u], 1);
-    const uint32_t last = u ? __shfl_sync(kAll, key[u ? u - 1 : 0], 31) : before;
-    if (lane == 0) prev = last;
-    const bool head = key[u] != prev;
-    heads[u] = __ballot_sync(kAll, head && use);
-    n += __popc(__ballot_sync(kAll, use));
-    const int x = 32 * u + lane;
-    if (head && x < nx) {
-      if (use) a.span[(int64_t)seg * L + key[u]].x = (int)(x0 + x);
-      if (x0 + x > 0 && prev < L) a.span[(int64_t)seg * L + prev].y = (int)(x0 + x);
-    }
-    if (use && x0 + x + 1 == a.w.per_head)
-      a.span[(int64_t)seg * L + key[u]].y = (int)(x0 + x + 1);
-  }
-  if (n == 0) return;
-
-  float dk[2 * NC][4], dv[2 * NC][4];
-  auto clear = [&]() {
-#pragma unroll
-    for (int t = 0; t < 2 * NC; ++t)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) dk[t][c] = dv[t][c] = 0.f;
-  };
-  clear();
-  uint32_t mykey = L;  // key of this lane's column pair; L: none
-  bool carried = (heads[0] & 1u) == 0;  // pair 0 began in an earlier range
-  int cur = -1;  // column pair of the last entry so far
-  if (carried) {
-    cur = 0;
-    if (tq == 0) mykey = before;
-  }
-  auto flush = [&]() {
-    if (mykey < L) {
-      float* o = carried && tq == 0
-          ? a.carry + ((int64_t)seg * a.w.ranges + range) * 2 * D
-          : a.top + ((int64_t)seg * L + mykey) * 2 * D;
-      o += 8 * (gr >> 1) + (gr & 1);
-#pragma unroll
-      for (int t = 0; t < 2 * NC; ++t)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int at = 32 * (t / 2) + 4 * (t & 1) + 2 * u;
-          o[at] = dk[t][2 * u] + dk[t][2 * u + 1];
-          o[D + at] = dv[t][2 * u] + dv[t][2 * u + 1];
-        }
-    }
-    mykey = L;
-    carried = false;
-  };
-
-#pragma unroll
-  for (int u = 0; u < NU; ++u) {
-#pragma unroll 1
-    for (int hf = 0; hf < 2; ++hf) {
-      const int g0 = 32 * u + 16 * hf;
-      if (g0 >= n) break;
-      const int cnt = min(16, n - g0);
-      // the rows of entries gr and gr + 8
-      const int ea = 16 * hf + gr;
-      const uint32_t rra = __shfl_sync(kAll, row[u], ea);
-      const uint32_t rrb = __shfl_sync(kAll, row[u], ea + 8);
-      const bool la = gr < cnt, lb = gr + 8 < cnt;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      uint4 qa[NC], qb[NC], ga[NP][NC], gb[NP][NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int64_t pa = (int64_t)rra * D + 32 * c;
-        const int64_t pb = (int64_t)rrb * D + 32 * c;
-        qa[c] = la ? __ldg(reinterpret_cast<const uint4*>(Q + pa)) : zero;
-        qb[c] = lb ? __ldg(reinterpret_cast<const uint4*>(Q + pb)) : zero;
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          ga[p][c] = la ? __ldg(reinterpret_cast<const uint4*>(G[p] + pa)) : zero;
-          gb[p][c] = lb ? __ldg(reinterpret_cast<const uint4*>(G[p] + pb)) : zero;
-        }
-      }
-      // weights of entries 2 tq, 2 tq + 1 and those + 8 (part gr & 1)
-      const int eb = 16 * hf + 2 * tq;
-      const int sh = (gr & 1) * 16;
-      uint32_t d0 = __shfl_sync(kAll, wd[u], eb) >> sh;
-      uint32_t d1 = __shfl_sync(kAll, wd[u], eb + 1) >> sh;
-      uint32_t d2 = __shfl_sync(kAll, wd[u], eb + 8) >> sh;
-      uint32_t d3 = __shfl_sync(kAll, wd[u], eb + 9) >> sh;
-      uint32_t p0 = __shfl_sync(kAll, wp[u], eb) >> sh;
-      uint32_t p1 = __shfl_sync(kAll, wp[u], eb + 1) >> sh;
-      uint32_t p2 = __shfl_sync(kAll, wp[u], eb + 8) >> sh;
-      uint32_t p3 = __shfl_sync(kAll, wp[u], eb + 9) >> sh;
-      const uint32_t hd = (heads[u] >> (16 * hf)) & 0xFFFFu;
-      uint32_t left = (1u << cnt) - 1u;  // entries still to be added
-      // usually once; again for each four keys when lists are short
-#pragma unroll 1
-      while (left) {
-        // place of each entry's key: cur + heads up to it among `left`
-        const uint32_t hl = hd & left;
-        const int me = lane & 15;
-        const int slot = cur + __popc(hl & ((2u << me) - 1u));
-        const bool act = lane < 16 && ((left >> me) & 1u) && slot < 4;
-        const uint32_t all = __ballot_sync(kAll, act);
-        uint32_t mt = 0, mn = 0;  // entries of this lane's pair, column
-        int top = cur;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t bm = __ballot_sync(kAll, act && slot == q);
-          if (q == tq) mt = bm;
-          if (q == (gr >> 1)) mn = bm;
-          if (bm) top = q;
-        }
-        const uint32_t kq =
-            __shfl_sync(kAll, key[u], 16 * hf + (mt ? __ffs(mt) - 1 : 0));
-        if (mt) mykey = kq;
-        cur = top;
-        const int e0 = 2 * tq;
-        const uint32_t z0 = ((mn >> e0) & 1u) ? 0xFFFFu : 0u;
-        const uint32_t z1 = ((mn >> (e0 + 1)) & 1u) ? 0xFFFFu : 0u;
-        const uint32_t z2 = ((mn >> (e0 + 8)) & 1u) ? 0xFFFFu : 0u;
-        const uint32_t z3 = ((mn >> (e0 + 9)) & 1u) ? 0xFFFFu : 0u;
-        const uint32_t D0 = (d0 & z0) | ((d1 & z1) << 16);
-        const uint32_t D1 = (d2 & z2) | ((d3 & z3) << 16);
-        const uint32_t P0 = (p0 & z0) | ((p1 & z1) << 16);
-        const uint32_t P1 = (p2 & z2) | ((p3 & z3) << 16);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          mma(dk[2 * c], transpose8x8(qa[c].x), transpose8x8(qa[c].y),
-              transpose8x8(qb[c].x), transpose8x8(qb[c].y), D0, D1);
-          mma(dk[2 * c + 1], transpose8x8(qa[c].z), transpose8x8(qa[c].w),
-              transpose8x8(qb[c].z), transpose8x8(qb[c].w), D0, D1);
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            mma(dv[2 * c], transpose8x8(ga[p][c].x), transpose8x8(ga[p][c].y),
-                transpose8x8(gb[p][c].x), transpose8x8(gb[p][c].y), P0, P1);
-            mma(dv[2 * c + 1], transpose8x8(ga[p][c].z),
-                transpose8x8(ga[p][c].w), transpose8x8(gb[p][c].z),
-                transpose8x8(gb[p][c].w), P0, P1);
-          }
-        }
-        left &= ~all;
-        if (left) {  // four keys are full: write them, go on with the next
-          flush();
-          clear();
-          cur = -1;
-        }
-      }
-    }
-  }
-  flush();
-}
-
 // ------------------------------------------------------------- column pass
 // A CTA owns 64 keys of one kv head, a warp 16: S^T and dP^T of 16 keys x 16
 // rows at a time, then dV += P^T dO and dK += dS^T Q with P^T and dS^T in two
@@ -881,20 +685,72 @@ backward_columns_mma(Args a, int ntile) {
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");  // K and V, if unused
-  // the listed part, then out
+  __syncthreads();
+  // The listed part: a key's first range (`top`) and the later ranges'
+  // shares (`carry`).  Up to kShort shares are added by the lanes that hold
+  // the key; longer runs (the anchor's spans nq G / kRange ranges) first by
+  // the whole CTA, in a fixed order.
+  constexpr int kShort = 4;
+  constexpr int kCols = 2 * D / 4, kParts = kColWarps * 32 / kCols;
+  int2* s_span = reinterpret_cast<int2*>(sQ);
+  float4* s_sum = reinterpret_cast<float4*>(sQ + 64 * 8);  // [parts][2 D]
+  if (threadIdx.x < 64)
+    s_span[threadIdx.x] = j0 + threadIdx.x < L
+                              ? a.span[(int64_t)seg * L + j0 + threadIdx.x]
+                              : make_int2(0, 0);
+  __syncthreads();
+#pragma unroll 1
+  for (int kl = 0; kl < 64; ++kl) {
+    const int2 sp = s_span[kl];
+    const int f = sp.x / kRange, e = (sp.y - 1) / kRange;
+    if (sp.y <= sp.x || e - f <= kShort) continue;  // the same for the CTA
+    const int c4 = threadIdx.x % kCols, part = threadIdx.x / kCols;
+    const float4* p = reinterpret_cast<const float4*>(
+                          a.carry + (int64_t)seg * a.w.ranges * 2 * D) + c4;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int r = f + 1 + part; r <= e; r += kParts) {
+      const float4 v = p[(int64_t)r * kCols];
+      t.x += v.x;
+      t.y += v.y;
+      t.z += v.z;
+      t.w += v.w;
+    }
+    s_sum[part * kCols + c4] = t;
+    __syncthreads();
+    if (kl >> 4 == wid && (kl & 7) == gr) {
+      const float* q = reinterpret_cast<const float*>(s_sum) + 2 * tq;
+      const int u = (kl >> 3) & 1;
+#pragma unroll
+      for (int part2 = 0; part2 < kParts; ++part2)
+#pragma unroll
+        for (int t2 = 0; t2 < NT; ++t2)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float k2 = q[part2 * 2 * D + 8 * t2 + c];
+            const float v2 = q[part2 * 2 * D + D + 8 * t2 + c];
+            dk[t2][c] += u ? 0.f : k2;
+            dk[t2][2 + c] += u ? k2 : 0.f;
+            dv[t2][c] += u ? 0.f : v2;
+            dv[t2][2 + c] += u ? v2 : 0.f;
+          }
+    }
+    __syncthreads();
+  }
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int j = kw + gr + 8 * u;
     if (j >= L) continue;
     const int64_t col = (int64_t)seg * L + j;
-    const int2 sp = a.span[col];
+    const int2 sp = s_span[wid * 16 + gr + 8 * u];
     if (sp.y > sp.x) {
-      const float* t0 = a.top + col * 2 * D + 2 * tq;
-      const int r1 = (sp.y - 1) / kRange;
-      for (int r = sp.x / kRange; r <= r1; ++r) {
-        const float* p = r == sp.x / kRange
-            ? t0
-            : a.carry + ((int64_t)seg * a.w.ranges + r) * 2 * D + 2 * tq;
+      const int f = sp.x / kRange, e = (sp.y - 1) / kRange;
+      const int r1 = e - f > kShort ? f : e;
+      for (int r = f; r <= r1; ++r) {
+        const float* p =
+            (r == f ? a.top + col * 2 * D
+                    : a.carry + ((int64_t)seg * a.w.ranges + r) * 2 * D) +
+            2 * tq;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const float2 k2 = *reinterpret_cast<const float2*>(p + 8 * t);
@@ -935,17 +791,6 @@ cudaError_t rows_as(const Args& a, cudaStream_t s) {
 }
 
 template <int D, int NP>
-cudaError_t listed_as(const Args& a, const uint32_t* keys,
-                      const uint32_t* ents, cudaStream_t s) {
-  prof_before(s, "backward_listed");
-  backward_listed_mma<D, NP>
-      <<<dim3((a.w.ranges + kListedWarps - 1) / kListedWarps, a.w.segs),
-         kListedWarps * 32, 0, s>>>(a, keys, ents);
-  prof_after(s);
-  return cudaGetLastError();
-}
-
-template <int D, int NP>
 cudaError_t columns_as(const Args& a, cudaStream_t s) {
   const int ntile = (a.L + 63) / 64;
   const int64_t ctas = (int64_t)a.w.segs * ntile;
@@ -964,15 +809,6 @@ cudaError_t columns_as(const Args& a, cudaStream_t s) {
 cudaError_t rows_mma_launch(const Args& a, int d, cudaStream_t s) {
   if (d == 64) return a.g[1] ? rows_as<64, 2>(a, s) : rows_as<64, 1>(a, s);
   return a.g[1] ? rows_as<128, 2>(a, s) : rows_as<128, 1>(a, s);
-}
-
-cudaError_t listed_mma_launch(const Args& a, int d, const uint32_t* keys,
-                              const uint32_t* ents, cudaStream_t s) {
-  if (d == 64)
-    return a.g[1] ? listed_as<64, 2>(a, keys, ents, s)
-                  : listed_as<64, 1>(a, keys, ents, s);
-  return a.g[1] ? listed_as<128, 2>(a, keys, ents, s)
-                : listed_as<128, 1>(a, keys, ents, s);
 }
 
 cudaError_t columns_mma_launch(const Args& a, int d, cudaStream_t s) {

@@ -11,14 +11,19 @@
 
 namespace ca {
 
-// N consecutive elements (a multiple of 16 bytes, 16-byte aligned) as floats.
+// N consecutive elements as floats: a multiple of 16 bytes (16-byte aligned),
+// or eight bytes of bf16.
 template <typename T, int N>
 __device__ __forceinline__ void load_row(const T* p, float* f) {
   constexpr int kPer = Elem<T>::kPer16B;
+  if constexpr (N < kPer) {
+    load_f32<T, N>(p, f);
+  } else {
 #pragma unroll
-  for (int v = 0; v < N / kPer; ++v) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + v);
-    Elem<T>::unpack(u, f + v * kPer);
+    for (int v = 0; v < N / kPer; ++v) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + v);
+      Elem<T>::unpack(u, f + v * kPer);
+    }
   }
 }
 

@@ -14,7 +14,7 @@ namespace ca {
 namespace bwd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSteps = kTile / kThreads;  // entries per thread
 
@@ -24,7 +24,7 @@ sort_count(Args a, const uint32_t* key, int shift, uint32_t mask) {
   const int64_t base = (int64_t)blockIdx.y * a.w.per_head;
   const int64_t e0 = (int64_t)blockIdx.x * kTile;
   const int n = (int)min((int64_t)kTile, a.w.per_head - e0);
-  cnt[threadIdx.x] = 0;
+  if (threadIdx.x < 256) cnt[threadIdx.x] = 0;
   uint32_t kv[kSteps];
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
@@ -37,8 +37,9 @@ sort_count(Args a, const uint32_t* key, int shift, uint32_t mask) {
     if (u * kThreads + threadIdx.x < n)
       atomicAdd(&cnt[(kv[u] >> shift) & mask], 1u);
   __syncthreads();
-  a.hist[((size_t)blockIdx.y * 256 + threadIdx.x) * a.w.tiles + blockIdx.x] =
-      cnt[threadIdx.x];
+  if (threadIdx.x < 256)
+    a.hist[((size_t)blockIdx.y * 256 + threadIdx.x) * a.w.tiles + blockIdx.x] =
+        cnt[threadIdx.x];
 }
 
 __device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane) {
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) sort_scan(Args a) {
   if (lane == 0) a.totals[at] = sum;
 }
 
-// Exclusive scan over the CTA's 256 threads.
+// Exclusive scan over the CTA's threads.
 __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t* s_warp) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const uint32_t x = warp_scan(v, lane);
@@ -85,10 +86,10 @@ __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t* s_warp) {
 // (equal digits of a step by lane, earlier steps by a running count), the
 // warps' counts are chained, and the tile, ordered by digit in shared
 // memory, goes out run by run.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 sort_place(Args a, const uint32_t* key, const uint32_t* ent, uint32_t* key_out,
            uint32_t* ent_out, int shift, uint32_t mask) {
-  __shared__ uint32_t cnt[kWarps][256];
+  __shared__ uint16_t cnt[kWarps][256];  // a tile has kTile <= 65535 entries
   __shared__ uint32_t s_key[kTile], s_ent[kTile];
   __shared__ uint32_t s_dst[256];  // global place of the tile's run, less its
                                    // local place
@@ -98,8 +99,8 @@ sort_place(Args a, const uint32_t* key, const uint32_t* ent, uint32_t* key_out,
   const int64_t t0 = (int64_t)blockIdx.x * kTile;
   const int n = (int)min((int64_t)kTile, a.w.per_head - t0);
   const int l0 = wid * (32 * kSteps);
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) cnt[w][threadIdx.x] = 0;
+  for (int c = threadIdx.x; c < kWarps * 256; c += kThreads)
+    (&cnt[0][0])[c] = 0;
   uint32_t kv[kSteps], ev[kSteps], rank[kSteps];
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
@@ -118,26 +119,30 @@ sort_place(Args a, const uint32_t* key, const uint32_t* ent, uint32_t* key_out,
     uint32_t before = 0;
     if (live) before = cnt[wid][dg];
     __syncwarp();
-    if (live && lower == 0) cnt[wid][dg] = before + __popc(same);
+    if (live && lower == 0) cnt[wid][dg] = (uint16_t)(before + __popc(same));
     __syncwarp();
     rank[u] = before + __popc(lower);
   }
   __syncthreads();
   {
-    const int dg = threadIdx.x;  // one digit per thread
+    const int dg = threadIdx.x;  // one digit per thread of the first 256
+    const bool mine = dg < 256;
+    const size_t at = (size_t)blockIdx.y * 256 + (mine ? dg : 0);
     uint32_t total = 0;
+    if (mine)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += cnt[w][dg];
+      for (int w = 0; w < kWarps; ++w) total += cnt[w][dg];
     const uint32_t local = cta_scan(total, s_warp);
-    const size_t at = (size_t)blockIdx.y * 256 + dg;
-    const uint32_t first = cta_scan(a.totals[at], s_warp);
-    s_dst[dg] = first + a.hist[at * a.w.tiles + blockIdx.x] - local;
-    uint32_t x = local;
+    const uint32_t first = cta_scan(mine ? a.totals[at] : 0u, s_warp);
+    if (mine) {
+      s_dst[dg] = first + a.hist[at * a.w.tiles + blockIdx.x] - local;
+      uint32_t x = local;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t c = cnt[w][dg];
-      cnt[w][dg] = x;
-      x += c;
+      for (int w = 0; w < kWarps; ++w) {
+        const uint32_t c = cnt[w][dg];
+        cnt[w][dg] = (uint16_t)x;
+        x += c;
+      }
     }
   }
   __syncthreads();
