@@ -82,26 +82,47 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t* hi,
 //   3. the window and the anchor again, now with the final log-sum-exp and
 //      D: dS, and dQ's window part.
 // The window is 5 blocks of 16 x 16 per 16 rows at W = 64, so computing its
-// scores twice costs less than keeping a second accumulator.
+// scores twice costs less than keeping a second accumulator.  What a warp
+// waits for is latency (a gathered row comes from L2): the index rows are
+// read in one batch, and the next V and K rows are asked for as soon as the
+// registers of the current ones are free.
 constexpr int kRowWarps = 4;
 
-template <int D>
+template <int D, int NP>
 struct RowSmem {
   static constexpr int CK = 64;         // keys staged at a time
   static constexpr int RS = D * 2 + 16; // padded row (bytes)
-  static constexpr size_t stage = (size_t)2 * CK * RS;  // K and V
-  static size_t per_warp(int k) {
-    const int kk = (k + 15) / 16 * 16;
+  // K and V of the window, or q and dO of the CTA's rows
+  static constexpr size_t stage = (size_t)(NP + 1) * 64 * RS;
+  __host__ __device__ static size_t per_warp(int kk) {
     return (size_t)16 * D * 4 + 4 * 16 * 4 + (size_t)kk * 8 +
            (size_t)16 * kk * 4;
   }
-  static size_t bytes(int k) { return stage + kRowWarps * per_warp(k); }
+  static size_t bytes(int k) {
+    return stage + kRowWarps * per_warp((k + 15) / 16 * 16);
+  }
+};
+
+// One gathered K or V row per four lanes, two per lane: keys gr and gr + 8.
+template <int D>
+struct Gather {
+  static constexpr int NC = D / 32;  // 64-byte pieces of a row
+  uint4 a[NC], b[NC];
+  __device__ __forceinline__ void load(const bf* base, int ja, int jb) {
+    const uint4* pa = reinterpret_cast<const uint4*>(base + (int64_t)ja * D);
+    const uint4* pb = reinterpret_cast<const uint4*>(base + (int64_t)jb * D);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      a[c] = __ldg(pa + 4 * c);
+      b[c] = __ldg(pb + 4 * c);
+    }
+  }
 };
 
 template <int D, int NP>
 __global__ void __launch_bounds__(kRowWarps * 32, D == 64 ? 4 : 2)
 backward_rows_mma(Args a, int ntile) {
-  using SM = RowSmem<D>;
+  using SM = RowSmem<D, NP>;
   constexpr int RS = SM::RS, CK = SM::CK;
   constexpr int KS = D / 16;  // steps of a product over the head dimension
   constexpr int NT = D / 8;   // its 8-wide tiles
@@ -123,10 +144,8 @@ backward_rows_mma(Args a, int ntile) {
   const bf* Vg = reinterpret_cast<const bf*>(a.V) + (int64_t)seg * L * D;
   unsigned char* sK = g_smem;
   unsigned char* sV = g_smem + (size_t)CK * RS;
-  float* s_dq = reinterpret_cast<float*>(
-      g_smem + SM::stage +
-      (size_t)wid * ((size_t)16 * D * 4 + 4 * 16 * 4 + (size_t)kk * 8 +
-                     (size_t)16 * kk * 4));
+  float* s_dq = reinterpret_cast<float*>(g_smem + SM::stage +
+                                         (size_t)wid * SM::per_warp(kk));
   float* s_m = s_dq + 16 * D;  // running maximum, then the log-sum-exp
   float* s_l = s_m + 16;
   float* s_E = s_l + 16;       // sum e dP, then D
@@ -134,22 +153,79 @@ backward_rows_mma(Args a, int ntile) {
   float2* s_xd = reinterpret_cast<float2*>(s_top + 16);  // one row's (x, dP)
   int* s_idx = reinterpret_cast<int*>(s_xd + kk);
   const float sl2 = kLog2e / sqrtf((float)D), sc = 1.f / sqrtf((float)D);
+  constexpr int kPieces = D * 2 / 16;  // 16-byte pieces of a row
 
+  // q and the planes of dO, rows r0 .. r0 + 63, where K and V are staged in
+  // the other phases
+  auto stage_rows = [&]() {
+    for (int e = threadIdx.x; e < 64 * kPieces; e += kRowWarps * 32) {
+      const int rr = e / kPieces, pc = e % kPieces;
+      const int64_t at = (int64_t)min(r0 + rr, nq - 1) * D + pc * 8;
+      unsigned char* dst = g_smem + rr * RS + pc * 16;
+      cp_async16(dst, Qg + at);
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        cp_async16(dst + (size_t)(p + 1) * 64 * RS, a.g[p] + rowbase * D + at);
+    }
+  };
+  stage_rows();
   if (threadIdx.x == 0) {
     s_kmin = 0x7FFFFFFF;
     s_any = 0;
   }
+
+  // the windows and Top-k counts of the warp's rows, a row per lane, and the
+  // Top-k positions: checked, kept, and written as the entries' sort keys
+  const int nrow = min(16, nq - i0);  // 0 or less: no rows
+  {
+    const int rr = min(lane, max(nrow, 1) - 1);
+    const int r = min(i0 + rr, nq - 1);
+    const bool mine = lane < nrow;
+    int w;
+    const int lo = window_lo(a, b, h, r, mine, &w);
+    const int m = listed_count(a, rowbase + r, a.p0 + r, lo, w, mine);
+    if (mine) s_top[lane] = m;
+    const int last = a.p0 + r - w;  // the last candidate
+    uint32_t* key = a.key[0] + (rowbase + i0) * (k + 1);
+    if (mine) key[(int64_t)lane * (k + 1)] = lo > 0 ? 0u : (uint32_t)L;
+    const int32_t* ix = a.idx + (rowbase + i0) * a.C_max + 1;
+#pragma unroll 1
+    for (int t0 = 0; t0 < k; t0 += 32) {
+      const int t = t0 + lane;
+      int j[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const int mu = __shfl_sync(kAll, m, u);
+        j[u] = u < nrow && t < mu ? __ldg(ix + (int64_t)u * a.C_max + t) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const int mu = __shfl_sync(kAll, m, u);
+        const int lu = __shfl_sync(kAll, last, u);
+        if (u < nrow && t < k) {
+          int v = j[u];
+          if (t < mu && (v < 1 || v > lu)) {  // not a candidate of this row
+            raise_flag(a.status, kErrCmax);
+            v = -1;
+          }
+          s_idx[u * kk + t] = v;
+          key[(int64_t)u * (k + 1) + 1 + t] = v < 0 ? (uint32_t)L : (uint32_t)v;
+        }
+      }
+    }
+  }
+  cp_async_wait_all();
   __syncthreads();
 
   // this lane's two rows of the warp's 16 in the window products
-  const bool wlive = i0 < nq;
+  const bool wlive = nrow > 0;
   const int ra = i0 + gr, rb = ra + 8;
   const bool va = ra < nq, vb = rb < nq;
   const int ca = min(ra, nq - 1), cb = min(rb, nq - 1);
   const int ia = a.p0 + ca, ib = a.p0 + cb;
   int wa, wb;
-  const int loa = window_lo(a, b, h, ca, va && tq == 0, &wa);
-  const int lob = window_lo(a, b, h, cb, vb && tq == 0, &wb);
+  const int loa = window_lo(a, b, h, ca, false, &wa);
+  const int lob = window_lo(a, b, h, cb, false, &wb);
   int kmin = min(loa, lob);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1)
@@ -160,33 +236,20 @@ backward_rows_mma(Args a, int ntile) {
     atomicMin(&s_kmin, kmin);
     if (anchors) s_any = 1;
   }
-
-  // the Top-k positions of the warp's rows: checked, kept, and written as
-  // the entries' sort keys
-#pragma unroll 1
-  for (int rr = 0; rr < 16 && i0 + rr < nq; ++rr) {
-    const int64_t row = rowbase + i0 + rr;
-    const int i = a.p0 + i0 + rr;
-    int w;
-    const int lo = window_lo(a, b, h, i0 + rr, false, &w);
-    const int m = listed_count(a, row, i, lo, w, lane == 0);
-    if (lane == 0) s_top[rr] = m;
-    uint32_t* key = a.key[0] + row * (k + 1);
-    const int32_t* ix = a.idx + row * a.C_max;
-    if (lane == 0) key[0] = lo > 0 ? 0u : (uint32_t)L;
-    for (int t = lane; t < k; t += 32) {
-      int j = -1;
-      if (t < m) {
-        j = __ldg(ix + 1 + t);
-        if (j < 1 || j > i - w) {  // not a candidate of this row
-          raise_flag(a.status, kErrCmax);
-          j = -1;
-        }
-      }
-      s_idx[rr * kk + t] = j;
-      key[1 + t] = j < 0 ? (uint32_t)L : (uint32_t)j;
+  // A operands of the window products: q and dO of the warp's rows
+  uint32_t qa[KS][4], ga[NP][KS][4];
+  auto fragments = [&]() {
+    const unsigned char* at =
+        g_smem + (wid * 16 + (lane & 15)) * RS + (lane >> 4) * 16;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      ldsm4(qa[ks], at + ks * 32);
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        ldsm4(ga[p][ks], at + (size_t)(p + 1) * 64 * RS + ks * 32);
     }
-  }
+  };
+  fragments();
   __syncthreads();
   const int cs0 = s_kmin & ~15;
   const int kmax_c = a.p0 + min(r0 + 63, nq - 1);
@@ -196,7 +259,6 @@ backward_rows_mma(Args a, int ntile) {
   auto stage = [&](int m) {
     const int cs = m < 0 ? 0 : cs0 + m * CK;
     const int rows = m < 0 ? 16 : min(CK, kmax_c + 1 - cs);
-    constexpr int kPieces = D * 2 / 16;
     for (int e = threadIdx.x; e < ((rows + 15) & ~15) * kPieces;
          e += kRowWarps * 32) {
       const int rr = e / kPieces, pc = e % kPieces;
@@ -208,8 +270,7 @@ backward_rows_mma(Args a, int ntile) {
   };
   // scores (log2 units, masked to -inf) and dP of the 16 x 16 block of keys
   // kb.. (at place kl of the staged chunk), as two accumulators of 8 keys
-  auto block = [&](const uint32_t (&qa)[KS][4], const uint32_t (&ga)[NP][KS][4],
-                   int kb, int kl, bool anchor, float (&x)[2][4],
+  auto block = [&](int kb, int kl, bool anchor, float (&x)[2][4],
                    float (&dp)[2][4]) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -247,25 +308,9 @@ backward_rows_mma(Args a, int ntile) {
         x[t][c] = ok ? x[t][c] * sl2 : -INFINITY;
       }
   };
-  auto fragments = [&](uint32_t (&qa)[KS][4], uint32_t (&ga)[NP][KS][4]) {
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int64_t at = (int64_t)((c & 1) ? cb : ca) * D + 16 * ks +
-                           2 * tq + (c >= 2 ? 8 : 0);
-        qa[ks][c] = __ldg(reinterpret_cast<const uint32_t*>(Qg + at));
-#pragma unroll
-        for (int p = 0; p < NP; ++p)
-          ga[p][ks][c] = __ldg(
-              reinterpret_cast<const uint32_t*>(a.g[p] + rowbase * D + at));
-      }
-  };
 
   // ---- 1: window and anchor, running sums
   {
-    uint32_t qa[KS][4], ga[NP][KS][4];
-    fragments(qa, ga);
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, E[2] = {0.f, 0.f};
 #pragma unroll 1
     for (int ch = m0; ch < nch; ++ch) {
@@ -277,7 +322,7 @@ backward_rows_mma(Args a, int ntile) {
 #pragma unroll 1
       for (int kb = jlo; wlive && kb <= jhi; kb += 16) {
         float x[2][4], dp[2][4];
-        block(qa, ga, kb, kb - cs, ch < 0, x, dp);
+        block(kb, kb - cs, ch < 0, x, dp);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const float mx = fmaxf(fmaxf(x[0][2 * u], x[0][2 * u + 1]),
@@ -301,6 +346,7 @@ backward_rows_mma(Args a, int ntile) {
       }
       __syncthreads();
     }
+    stage_rows();  // for the Top-k and the last phase
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       float mx = m[u];
@@ -318,150 +364,166 @@ backward_rows_mma(Args a, int ntile) {
         s_E[gr + 8 * u] = EE;
       }
     }
-    __syncwarp();
+    cp_async_wait_all();
+    __syncthreads();
   }
 
-  // ---- 2: the Top-k, row by row
-#pragma unroll 1
-  for (int rr = 0; rr < 16 && i0 + rr < nq; ++rr) {
-    const int64_t row = rowbase + i0 + rr;
-    const int mt = s_top[rr];
-    float m = s_m[rr], l0 = s_l[rr], E0 = s_E[rr];  // window and anchor
-    float l = 0.f, E = 0.f;  // this lane's keys
-    uint4 qv[NC], gv[NP][NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t at = row * D + 32 * c + 8 * tq;
-      qv[c] = __ldg(reinterpret_cast<const uint4*>(
-          reinterpret_cast<const bf*>(a.Q) + at));
-#pragma unroll
-      for (int p = 0; p < NP; ++p)
-        gv[p][c] = __ldg(reinterpret_cast<const uint4*>(a.g[p] + at));
+  // ---- 2: the Top-k, row by row, 16 entries at a time
+  {
+    const bf* Kl = Kg + 8 * tq;
+    const bf* Vl = Vg + 8 * tq;
+    Gather<D> kr, vr;
+    int ja = -1, jb = -1;  // the entries in kr and vr (-1: none, row 0 read)
+    auto entries = [&](int rr, int g0, int* pa, int* pb) {
+      const int mt = s_top[rr];
+      *pa = g0 + gr < mt ? s_idx[rr * kk + g0 + gr] : -1;
+      *pb = g0 + gr + 8 < mt ? s_idx[rr * kk + g0 + gr + 8] : -1;
+    };
+    if (wlive && s_top[0] > 0) {
+      entries(0, 0, &ja, &jb);
+      kr.load(Kl, max(ja, 0), max(jb, 0));
+      vr.load(Vl, max(ja, 0), max(jb, 0));
     }
-    float acc[2 * NC][4];
-#pragma unroll
-    for (int t = 0; t < 2 * NC; ++t)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[t][c] = 0.f;
 #pragma unroll 1
-    for (int g0 = 0; g0 < mt; g0 += 16) {
-      const int ja = g0 + gr < mt ? s_idx[rr * kk + g0 + gr] : -1;
-      const int jb = g0 + gr + 8 < mt ? s_idx[rr * kk + g0 + gr + 8] : -1;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      uint4 ka[NC], kb[NC], vva[NC], vvb[NC];
+    for (int rr = 0; rr < nrow; ++rr) {
+      const int64_t row = rowbase + i0 + rr;
+      const int mt = s_top[rr];
+      float m = s_m[rr], l0 = s_l[rr], E0 = s_E[rr];  // window and anchor
+      float l = 0.f, E = 0.f;  // this lane's keys
+      const unsigned char* qrow = g_smem + (wid * 16 + rr) * RS + 16 * tq;
+      float acc[2 * NC][4];
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int64_t pa = (int64_t)ja * D + 32 * c + 8 * tq;
-        const int64_t pb = (int64_t)jb * D + 32 * c + 8 * tq;
-        ka[c] = ja >= 0 ? __ldg(reinterpret_cast<const uint4*>(Kg + pa)) : zero;
-        kb[c] = jb >= 0 ? __ldg(reinterpret_cast<const uint4*>(Kg + pb)) : zero;
-        vva[c] = ja >= 0 ? __ldg(reinterpret_cast<const uint4*>(Vg + pa)) : zero;
-        vvb[c] = jb >= 0 ? __ldg(reinterpret_cast<const uint4*>(Vg + pb)) : zero;
-      }
-      float x[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < 2 * NC; ++t)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        mma(x, ka[c].x, kb[c].x, ka[c].y, kb[c].y, qv[c].x, qv[c].y);
-        mma(x, ka[c].z, kb[c].z, ka[c].w, kb[c].w, qv[c].z, qv[c].w);
-      }
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          mma(dp, vva[c].x, vvb[c].x, vva[c].y, vvb[c].y, gv[p][c].x,
-              gv[p][c].y);
-          mma(dp, vva[c].z, vvb[c].z, vva[c].w, vvb[c].w, gv[p][c].z,
-              gv[p][c].w);
+        for (int c = 0; c < 4; ++c) acc[t][c] = 0.f;
+      if (mt == 0 && rr + 1 < nrow) {  // nothing was read for this row
+        entries(rr + 1, 0, &ja, &jb);
+        if (s_top[rr + 1] > 0) {
+          kr.load(Kl, max(ja, 0), max(jb, 0));
+          vr.load(Vl, max(ja, 0), max(jb, 0));
         }
-      // keys gr and gr + 8, the same in all four lanes of a row
-      const float xa = ja >= 0 ? x[0] * sl2 : -INFINITY;
-      const float xb = jb >= 0 ? x[2] * sl2 : -INFINITY;
-      float mx = fmaxf(xa, xb);
-#pragma unroll
-      for (int off = 4; off <= 16; off <<= 1)
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, off));
-      if (mx > m) {  // the same for the whole warp
-        const float f = exp2f(m - mx);
-        l0 *= f;
-        E0 *= f;
-        l *= f;
-        E *= f;
-#pragma unroll
-        for (int t = 0; t < 2 * NC; ++t)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[t][c] *= f;
-        m = mx;
       }
-      const float ea = exp2f(xa - m), eb = exp2f(xb - m);
-      l += ea + eb;
-      E = fmaf(ea, dp[0], fmaf(eb, dp[2], E));
-      if (tq == 0) {
-        s_xd[g0 + gr] = make_float2(xa, dp[0]);
-        s_xd[g0 + gr + 8] = make_float2(xb, dp[2]);
-      }
-      // B: columns 0, 1 = e dP (hi, lo), 2, 3 = e (hi, lo), 4..7 zero; this
-      // lane's are keys 2 tq, 2 tq + 1, and those + 8, of column gr
-      const float sa = (tq & 1) ? ea : ea * dp[0];
-      const float sb = (tq & 1) ? eb : eb * dp[2];
-      const int src = 8 * tq + ((gr >> 1) & 1);
-      float b00 = __shfl_sync(kAll, sa, src), b01 = __shfl_sync(kAll, sa, src + 4);
-      float b10 = __shfl_sync(kAll, sb, src), b11 = __shfl_sync(kAll, sb, src + 4);
-      uint32_t bhi0, blo0, bhi1, blo1;
-      split2(b00, b01, &bhi0, &blo0);
-      split2(b10, b11, &bhi1, &blo1);
-      const uint32_t B0 = gr >= 4 ? 0u : (gr & 1) ? blo0 : bhi0;
-      const uint32_t B1 = gr >= 4 ? 0u : (gr & 1) ? blo1 : bhi1;
+#pragma unroll 1
+      for (int g0 = 0; g0 < mt; g0 += 16) {
+        // the next entries: of this row, or the first of the next one
+        int na, nb;
+        {
+          const bool same = g0 + 16 < mt;
+          entries(same ? rr : min(rr + 1, nrow - 1), same ? g0 + 16 : 0, &na,
+                  &nb);
+        }
+        float x[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        mma(acc[2 * c], transpose8x8(ka[c].x), transpose8x8(ka[c].y),
-            transpose8x8(kb[c].x), transpose8x8(kb[c].y), B0, B1);
-        mma(acc[2 * c + 1], transpose8x8(ka[c].z), transpose8x8(ka[c].w),
-            transpose8x8(kb[c].z), transpose8x8(kb[c].w), B0, B1);
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const uint4 g = *reinterpret_cast<const uint4*>(
+                qrow + (size_t)(p + 1) * 64 * RS + 64 * c);
+            mma(dp, vr.a[c].x, vr.b[c].x, vr.a[c].y, vr.b[c].y, g.x, g.y);
+            mma(dp, vr.a[c].z, vr.b[c].z, vr.a[c].w, vr.b[c].w, g.z, g.w);
+          }
+        vr.load(Vl, max(na, 0), max(nb, 0));
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const uint4 q = *reinterpret_cast<const uint4*>(qrow + 64 * c);
+          mma(x, kr.a[c].x, kr.b[c].x, kr.a[c].y, kr.b[c].y, q.x, q.y);
+          mma(x, kr.a[c].z, kr.b[c].z, kr.a[c].w, kr.b[c].w, q.z, q.w);
+        }
+        // keys gr and gr + 8, the same in all four lanes of a row
+        const float xa = ja >= 0 ? x[0] * sl2 : -INFINITY;
+        const float xb = jb >= 0 ? x[2] * sl2 : -INFINITY;
+        float mx = fmaxf(xa, xb);
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1)
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, off));
+        if (mx > m) {  // the same for the whole warp
+          const float f = exp2f(m - mx);
+          l0 *= f;
+          E0 *= f;
+          l *= f;
+          E *= f;
+#pragma unroll
+          for (int t = 0; t < 2 * NC; ++t)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[t][c] *= f;
+          m = mx;
+        }
+        const float ea = exp2f(xa - m), eb = exp2f(xb - m);
+        l += ea + eb;
+        E = fmaf(ea, dp[0], fmaf(eb, dp[2], E));
+        if (tq == 0) {
+          s_xd[g0 + gr] = make_float2(xa, dp[0]);
+          s_xd[g0 + gr + 8] = make_float2(xb, dp[2]);
+        }
+        // B: columns 0, 1 = e dP (hi, lo), 2, 3 = e (hi, lo), 4..7 zero; this
+        // lane's are keys 2 tq, 2 tq + 1, and those + 8, of column gr
+        const float sa = (tq & 1) ? ea : ea * dp[0];
+        const float sb = (tq & 1) ? eb : eb * dp[2];
+        const int src = 8 * tq + ((gr >> 1) & 1);
+        float b00 = __shfl_sync(kAll, sa, src);
+        float b01 = __shfl_sync(kAll, sa, src + 4);
+        float b10 = __shfl_sync(kAll, sb, src);
+        float b11 = __shfl_sync(kAll, sb, src + 4);
+        uint32_t bhi0, blo0, bhi1, blo1;
+        split2(b00, b01, &bhi0, &blo0);
+        split2(b10, b11, &bhi1, &blo1);
+        const uint32_t B0 = gr >= 4 ? 0u : (gr & 1) ? blo0 : bhi0;
+        const uint32_t B1 = gr >= 4 ? 0u : (gr & 1) ? blo1 : bhi1;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          mma(acc[2 * c], transpose8x8(kr.a[c].x), transpose8x8(kr.a[c].y),
+              transpose8x8(kr.b[c].x), transpose8x8(kr.b[c].y), B0, B1);
+          mma(acc[2 * c + 1], transpose8x8(kr.a[c].z), transpose8x8(kr.a[c].w),
+              transpose8x8(kr.b[c].z), transpose8x8(kr.b[c].w), B0, B1);
+        }
+        kr.load(Kl, max(na, 0), max(nb, 0));
+        ja = na;
+        jb = nb;
       }
+#pragma unroll
+      for (int off = 4; off <= 16; off <<= 1) {
+        l += __shfl_xor_sync(kAll, l, off);
+        E += __shfl_xor_sync(kAll, E, off);
+      }
+      l += l0;
+      E += E0;
+      const float inv = 1.f / l, Di = E * inv, lse = m + log2f(l);
+      if (lane == 0) {
+        s_m[rr] = lse;
+        s_E[rr] = Di;
+        a.stats[row] = make_float2(lse, Di);
+      }
+      // lanes tq = 0 hold A, tq = 1 Bk, of dimensions 32 c + 8 (gr / 2) +
+      // gr % 2 + {0, 2, 4, 6}
+#pragma unroll
+      for (int t = 0; t < 2 * NC; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float v = acc[t][2 * u] + acc[t][2 * u + 1];
+          const float o = __shfl_down_sync(kAll, v, 1);
+          if (tq == 0)
+            s_dq[rr * D + 32 * (t / 2) + 8 * (gr >> 1) + (gr & 1) +
+                 4 * (t & 1) + 2 * u] = (v - Di * o) * inv * sc;
+        }
+      __syncwarp();
+      float2* pds = a.pds + row * (k + 1);
+      for (int t = lane; t < k; t += 32) {
+        float2 o = make_float2(0.f, 0.f);
+        if (t < mt) {
+          const float2 xd = s_xd[t];
+          o.x = exp2f(xd.x - lse);  // 0 where the slot was refused
+          o.y = o.x * (xd.y - Di) * sc;
+        }
+        pds[1 + t] = o;
+      }
+      __syncwarp();
     }
-#pragma unroll
-    for (int off = 4; off <= 16; off <<= 1) {
-      l += __shfl_xor_sync(kAll, l, off);
-      E += __shfl_xor_sync(kAll, E, off);
-    }
-    l += l0;
-    E += E0;
-    const float inv = 1.f / l, Di = E * inv, lse = m + log2f(l);
-    if (lane == 0) {
-      s_m[rr] = lse;
-      s_E[rr] = Di;
-      a.stats[row] = make_float2(lse, Di);
-    }
-    // lanes tq = 0 hold A, tq = 1 Bk, of dimensions 32 c + 8 (gr / 2) +
-    // gr % 2 + {0, 2, 4, 6}
-#pragma unroll
-    for (int t = 0; t < 2 * NC; ++t)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float v = acc[t][2 * u] + acc[t][2 * u + 1];
-        const float o = __shfl_down_sync(kAll, v, 1);
-        if (tq == 0)
-          s_dq[rr * D + 32 * (t / 2) + 8 * (gr >> 1) + (gr & 1) + 4 * (t & 1) +
-               2 * u] = (v - Di * o) * inv * sc;
-      }
-    __syncwarp();
-    float2* pds = a.pds + row * (k + 1);
-    for (int t = lane; t < k; t += 32) {
-      float2 o = make_float2(0.f, 0.f);
-      if (t < mt) {
-        const float2 xd = s_xd[t];
-        o.x = exp2f(xd.x - lse);  // 0 where the slot was refused
-        o.y = o.x * (xd.y - Di) * sc;
-      }
-      pds[1 + t] = o;
-    }
-    __syncwarp();
   }
 
   // ---- 3: dS of the window and the anchor
   {
-    uint32_t qa[KS][4], ga[NP][KS][4];
-    fragments(qa, ga);
+    fragments();
+    __syncthreads();
     float o[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -478,7 +540,7 @@ backward_rows_mma(Args a, int ntile) {
 #pragma unroll 1
       for (int kb = jlo; wlive && kb <= jhi; kb += 16) {
         float x[2][4], dp[2][4];
-        block(qa, ga, kb, kb - cs, ch < 0, x, dp);
+        block(kb, kb - cs, ch < 0, x, dp);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -495,12 +557,12 @@ backward_rows_mma(Args a, int ntile) {
         split2(x[0][2], x[0][3], &hi[1], &lo[1]);
         split2(x[1][0], x[1][1], &hi[2], &lo[2]);
         split2(x[1][2], x[1][3], &hi[3], &lo[3]);
-        const unsigned char* kr = sK + (kb - cs + (lane & 15)) * RS +
+        const unsigned char* kp = sK + (kb - cs + (lane & 15)) * RS +
                                   (lane >> 4) * 16;
 #pragma unroll
         for (int t = 0; t < NT; t += 2) {
           uint32_t f[4];
-          ldsm4t(f, kr + t * 16);
+          ldsm4t(f, kp + t * 16);
           mma(o[t], hi[0], hi[1], hi[2], hi[3], f[0], f[1]);
           mma(o[t], lo[0], lo[1], lo[2], lo[3], f[0], f[1]);
           mma(o[t + 1], hi[0], hi[1], hi[2], hi[3], f[2], f[3]);
@@ -520,10 +582,9 @@ backward_rows_mma(Args a, int ntile) {
       pb[1] += o[t][3];
     }
     __syncwarp();
-    constexpr int kPieces = D / 8;
     bf* dQ = reinterpret_cast<bf*>(a.dQ) + (rowbase + i0) * D;
-    for (int e = lane; e < 16 * kPieces; e += 32)
-      if (i0 + e / kPieces < nq)
+    for (int e = lane; e < 16 * (D / 8); e += 32)
+      if (e / (D / 8) < nrow)
         reinterpret_cast<uint4*>(dQ)[e] = pack16<bf>(s_dq + e * 8);
   }
 }
@@ -780,7 +841,7 @@ cudaError_t rows_as(const Args& a, cudaStream_t s) {
   const int ntile = (a.nq + 63) / 64;
   const int64_t ctas = (int64_t)a.B * a.Hq * ntile;
   if (ctas > 0x7FFFFFFF) return cudaErrorNotSupported;
-  const size_t smem = RowSmem<D>::bytes(a.k);
+  const size_t smem = RowSmem<D, NP>::bytes(a.k);
   auto kern = backward_rows_mma<D, NP>;
   cudaError_t e = ensure_smem(kern, smem);
   if (e != cudaSuccess) return e;
