@@ -72,13 +72,13 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t* hi,
 // A CTA owns 64 query rows of one head, a warp 16.  In order:
 //   1. the window's and the anchor's scores and dP: running (max, sum e,
 //      sum e dP) of each row;
-//   2. row by row, the Top-k: 16 gathered K and V rows at a time are the A
-//      operand of a product with q and dO (every column of B the same), so
-//      the score of key r lies in the lanes that hold its row.  The sums
-//      A = sum e dP k and Bk = sum e k take the same K registers, transposed
-//      in place, against a B operand whose columns are e dP and e in two
-//      parts each.  So a gathered row is read once, and dQ's listed part
-//      (A - D Bk) / l follows when the row's sums are complete;
+//   2. row by row, the Top-k, 16 gathered K and V rows at a time: as A
+//      operands they meet q and dO, half lines as rows of A against half
+//      lines as columns of B.  The sums A = sum e dP k and Bk = sum e k take
+//      the same K registers, transposed in place, against a B operand whose
+//      columns are e dP and e in two parts each.  So a gathered row is read
+//      once, and dQ's listed part (A - D Bk) / l follows when the row's sums
+//      are complete;
 //   3. the window and the anchor again, now with the final log-sum-exp and
 //      D: dS, and dQ's window part.
 // The window is 5 blocks of 16 x 16 per 16 rows at W = 64, so computing its
@@ -103,21 +103,70 @@ struct RowSmem {
   }
 };
 
-// One gathered K or V row per four lanes, two per lane: keys gr and gr + 8.
+// 16 gathered K or V rows: load i holds keys 4 i + gr / 2, eight lanes on one
+// 128-byte line (four wavefronts a load; rows spread over four lanes each
+// took eight).
 template <int D>
 struct Gather {
-  static constexpr int NC = D / 32;  // 64-byte pieces of a row
-  uint4 a[NC], b[NC];
-  __device__ __forceinline__ void load(const bf* base, int ja, int jb) {
-    const uint4* pa = reinterpret_cast<const uint4*>(base + (int64_t)ja * D);
-    const uint4* pb = reinterpret_cast<const uint4*>(base + (int64_t)jb * D);
+  static constexpr int NL = D / 64;  // lines of a row
+  uint32_t v[4][NL][4];
+  __device__ __forceinline__ void load(const bf* base, const int (&j)[4]) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      a[c] = __ldg(pa + 4 * c);
-      b[c] = __ldg(pb + 4 * c);
+    for (int i = 0; i < 4; ++i) {
+      const uint4* p =
+          reinterpret_cast<const uint4*>(base + (int64_t)max(j[i], 0) * D);
+#pragma unroll
+      for (int c = 0; c < NL; ++c) {
+        const uint4 t = __ldg(p + 8 * c);
+        v[i][c][0] = t.x;
+        v[i][c][1] = t.y;
+        v[i][c][2] = t.z;
+        v[i][c][3] = t.w;
+      }
     }
   }
+  // Products of all rows with a vector whose halves of each line stand in
+  // the even and odd columns of B (w: this lane's 16 bytes of a line).  The
+  // result for key 4 tq + gr / 2.
+  __device__ __forceinline__ float dot(const uint4 (&w)[NL], int gr,
+                                       int tq) const {
+    float d[2][4];
+    add_dot(w, d, true);
+    return pick(d, gr, tq);
+  }
+  __device__ __forceinline__ void add_dot(const uint4 (&w)[NL],
+                                          float (&d)[2][4], bool clear) const {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      if (clear) d[g][0] = d[g][1] = d[g][2] = d[g][3] = 0.f;
+#pragma unroll
+      for (int c = 0; c < NL; ++c) {
+        mma(d[g], v[2 * g][c][0], v[2 * g + 1][c][0], v[2 * g][c][1],
+            v[2 * g + 1][c][1], w[c].x, w[c].y);
+        mma(d[g], v[2 * g][c][2], v[2 * g + 1][c][2], v[2 * g][c][3],
+            v[2 * g + 1][c][3], w[c].z, w[c].w);
+      }
+    }
+  }
+  // Row gr (and gr + 8) of a product is key gr / 2 of a load, its first half
+  // at even gr (even columns), its second at odd gr (odd columns).
+  __device__ __forceinline__ static float pick(const float (&d)[2][4], int gr,
+                                               int tq) {
+    const bool odd = gr & 1;
+    const float a0 = odd ? d[0][1] : d[0][0], a1 = odd ? d[0][3] : d[0][2];
+    const float b0 = odd ? d[1][1] : d[1][0], b1 = odd ? d[1][3] : d[1][2];
+    const float a = (tq & 1) ? a1 : a0, b = (tq & 1) ? b1 : b0;
+    const float x = (tq & 2) ? b : a;
+    return x + __shfl_xor_sync(kAll, x, 4);
+  }
 };
+
+// The largest of the warp's values.
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 template <int D, int NP>
 __global__ void __launch_bounds__(kRowWarps * 32, D == 64 ? 4 : 2)
@@ -126,7 +175,6 @@ backward_rows_mma(Args a, int ntile) {
   constexpr int RS = SM::RS, CK = SM::CK;
   constexpr int KS = D / 16;  // steps of a product over the head dimension
   constexpr int NT = D / 8;   // its 8-wide tiles
-  constexpr int NC = D / 32;  // 64-byte pieces of a row
   extern __shared__ __align__(16) unsigned char g_smem[];
   __shared__ int s_kmin, s_any;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -370,139 +418,134 @@ backward_rows_mma(Args a, int ntile) {
 
   // ---- 2: the Top-k, row by row, 16 entries at a time
   {
-    const bf* Kl = Kg + 8 * tq;
-    const bf* Vl = Vg + 8 * tq;
+    constexpr int NL = D / 64;
+    const bf* Kl = Kg + 8 * (lane & 7);
+    const bf* Vl = Vg + 8 * (lane & 7);
+    const int half = gr & 1, kq = gr >> 1;
     Gather<D> kr, vr;
-    int ja = -1, jb = -1;  // the entries in kr and vr (-1: none, row 0 read)
-    auto entries = [&](int rr, int g0, int* pa, int* pb) {
+    int j[4];  // the entries in kr and vr (-1: none, row 0 is read)
+    auto entries = [&](int rr, int g0) {
       const int mt = s_top[rr];
-      *pa = g0 + gr < mt ? s_idx[rr * kk + g0 + gr] : -1;
-      *pb = g0 + gr + 8 < mt ? s_idx[rr * kk + g0 + gr + 8] : -1;
+      const int* ix = s_idx + rr * kk + g0 + kq;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) j[i] = g0 + 4 * i + kq < mt ? ix[4 * i] : -1;
     };
     if (wlive && s_top[0] > 0) {
-      entries(0, 0, &ja, &jb);
-      kr.load(Kl, max(ja, 0), max(jb, 0));
-      vr.load(Vl, max(ja, 0), max(jb, 0));
+      entries(0, 0);
+      kr.load(Kl, j);
+      vr.load(Vl, j);
     }
 #pragma unroll 1
     for (int rr = 0; rr < nrow; ++rr) {
       const int64_t row = rowbase + i0 + rr;
       const int mt = s_top[rr];
       float m = s_m[rr], l0 = s_l[rr], E0 = s_E[rr];  // window and anchor
-      float l = 0.f, E = 0.f;  // this lane's keys
-      const unsigned char* qrow = g_smem + (wid * 16 + rr) * RS + 16 * tq;
-      float acc[2 * NC][4];
+      // even columns: first halves of the lines, odd columns: second halves
+      const unsigned char* qrow =
+          g_smem + (wid * 16 + rr) * RS + 64 * half + 16 * tq;
+      // sums: acc of the rows' dimensions, sum of the weights alone (columns
+      // 0, 1: e dP, columns 2, 3: e)
+      float acc[2 * NL][4], sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int t = 0; t < 2 * NC; ++t)
+      for (int t = 0; t < 2 * NL; ++t)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[t][c] = 0.f;
-      if (mt == 0 && rr + 1 < nrow) {  // nothing was read for this row
-        entries(rr + 1, 0, &ja, &jb);
-        if (s_top[rr + 1] > 0) {
-          kr.load(Kl, max(ja, 0), max(jb, 0));
-          vr.load(Vl, max(ja, 0), max(jb, 0));
-        }
+      if (mt == 0 && rr + 1 < nrow && s_top[rr + 1] > 0) {
+        entries(rr + 1, 0);  // nothing was read ahead
+        kr.load(Kl, j);
+        vr.load(Vl, j);
       }
 #pragma unroll 1
       for (int g0 = 0; g0 < mt; g0 += 16) {
+        // this lane's key of the softmax: 4 tq + gr / 2
+        const int mine = g0 + 4 * tq + kq;
+        const bool use = mine < mt && s_idx[rr * kk + mine] >= 0;
         // the next entries: of this row, or the first of the next one
-        int na, nb;
+        const bool same = g0 + 16 < mt;
+        entries(same ? rr : min(rr + 1, nrow - 1), same ? g0 + 16 : 0);
+        float d[2][4];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          uint4 w[NL];
+#pragma unroll
+          for (int c = 0; c < NL; ++c)
+            w[c] = *reinterpret_cast<const uint4*>(
+                qrow + (size_t)(p + 1) * 64 * RS + 128 * c);
+          vr.add_dot(w, d, p == 0);
+        }
+        vr.load(Vl, j);
+        const float dp = Gather<D>::pick(d, gr, tq);
+        float x;
         {
-          const bool same = g0 + 16 < mt;
-          entries(same ? rr : min(rr + 1, nrow - 1), same ? g0 + 16 : 0, &na,
-                  &nb);
+          uint4 w[NL];
+#pragma unroll
+          for (int c = 0; c < NL; ++c)
+            w[c] = *reinterpret_cast<const uint4*>(qrow + 128 * c);
+          x = kr.dot(w, gr, tq);
         }
-        float x[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int p = 0; p < NP; ++p)
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const uint4 g = *reinterpret_cast<const uint4*>(
-                qrow + (size_t)(p + 1) * 64 * RS + 64 * c);
-            mma(dp, vr.a[c].x, vr.b[c].x, vr.a[c].y, vr.b[c].y, g.x, g.y);
-            mma(dp, vr.a[c].z, vr.b[c].z, vr.a[c].w, vr.b[c].w, g.z, g.w);
-          }
-        vr.load(Vl, max(na, 0), max(nb, 0));
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const uint4 q = *reinterpret_cast<const uint4*>(qrow + 64 * c);
-          mma(x, kr.a[c].x, kr.b[c].x, kr.a[c].y, kr.b[c].y, q.x, q.y);
-          mma(x, kr.a[c].z, kr.b[c].z, kr.a[c].w, kr.b[c].w, q.z, q.w);
-        }
-        // keys gr and gr + 8, the same in all four lanes of a row
-        const float xa = ja >= 0 ? x[0] * sl2 : -INFINITY;
-        const float xb = jb >= 0 ? x[2] * sl2 : -INFINITY;
-        float mx = fmaxf(xa, xb);
-#pragma unroll
-        for (int off = 4; off <= 16; off <<= 1)
-          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, off));
+        x = use ? x * sl2 : -INFINITY;
+        const float mx = warp_max(x);
         if (mx > m) {  // the same for the whole warp
           const float f = exp2f(m - mx);
           l0 *= f;
           E0 *= f;
-          l *= f;
-          E *= f;
 #pragma unroll
-          for (int t = 0; t < 2 * NC; ++t)
+          for (int c = 0; c < 4; ++c) sum[c] *= f;
+#pragma unroll
+          for (int t = 0; t < 2 * NL; ++t)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[t][c] *= f;
           m = mx;
         }
-        const float ea = exp2f(xa - m), eb = exp2f(xb - m);
-        l += ea + eb;
-        E = fmaf(ea, dp[0], fmaf(eb, dp[2], E));
-        if (tq == 0) {
-          s_xd[g0 + gr] = make_float2(xa, dp[0]);
-          s_xd[g0 + gr + 8] = make_float2(xb, dp[2]);
-        }
-        // B: columns 0, 1 = e dP (hi, lo), 2, 3 = e (hi, lo), 4..7 zero; this
-        // lane's are keys 2 tq, 2 tq + 1, and those + 8, of column gr
-        const float sa = (tq & 1) ? ea : ea * dp[0];
-        const float sb = (tq & 1) ? eb : eb * dp[2];
-        const int src = 8 * tq + ((gr >> 1) & 1);
-        float b00 = __shfl_sync(kAll, sa, src);
-        float b01 = __shfl_sync(kAll, sa, src + 4);
-        float b10 = __shfl_sync(kAll, sb, src);
-        float b11 = __shfl_sync(kAll, sb, src + 4);
-        uint32_t bhi0, blo0, bhi1, blo1;
-        split2(b00, b01, &bhi0, &blo0);
-        split2(b10, b11, &bhi1, &blo1);
-        const uint32_t B0 = gr >= 4 ? 0u : (gr & 1) ? blo0 : bhi0;
-        const uint32_t B1 = gr >= 4 ? 0u : (gr & 1) ? blo1 : bhi1;
+        const float e = exp2f(x - m);
+        if (half == 0) s_xd[mine] = make_float2(x, dp);
+        // B: columns 0-3 (4-7) weigh the rows' first (second) halves with
+        // e dP (hi, lo) and e (hi, lo); its row pair (2 tq, 2 tq + 1) is the
+        // two halves of key tq of a load
+        const float w = half ? e : e * dp;
+        const int src = 8 * tq + 4 * ((gr >> 1) & 1);
+        uint32_t B[4];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          mma(acc[2 * c], transpose8x8(kr.a[c].x), transpose8x8(kr.a[c].y),
-              transpose8x8(kr.b[c].x), transpose8x8(kr.b[c].y), B0, B1);
-          mma(acc[2 * c + 1], transpose8x8(kr.a[c].z), transpose8x8(kr.a[c].w),
-              transpose8x8(kr.b[c].z), transpose8x8(kr.b[c].w), B0, B1);
+        for (int i = 0; i < 4; ++i) {
+          const float v = __shfl_sync(kAll, w, src + i);
+          const uint32_t hi = pack2(v, 0.f);
+          const uint32_t t = half ? pack2(v - bf16lo(hi), 0.f) : hi;
+          B[i] = gr >= 4 ? t << 16 : t;
         }
-        kr.load(Kl, max(na, 0), max(nb, 0));
-        ja = na;
-        jb = nb;
-      }
+        constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones
+        mma(sum, kOnes, kOnes, kOnes, kOnes, B[0], B[1]);
+        mma(sum, kOnes, kOnes, kOnes, kOnes, B[2], B[3]);
 #pragma unroll
-      for (int off = 4; off <= 16; off <<= 1) {
-        l += __shfl_xor_sync(kAll, l, off);
-        E += __shfl_xor_sync(kAll, E, off);
+        for (int c = 0; c < NL; ++c)
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              mma(acc[2 * c + t], transpose8x8(kr.v[2 * g][c][2 * t]),
+                  transpose8x8(kr.v[2 * g][c][2 * t + 1]),
+                  transpose8x8(kr.v[2 * g + 1][c][2 * t]),
+                  transpose8x8(kr.v[2 * g + 1][c][2 * t + 1]), B[2 * g],
+                  B[2 * g + 1]);
+        kr.load(Kl, j);
       }
-      l += l0;
-      E += E0;
+      const float l = l0 + __shfl_sync(kAll, sum[0] + sum[1], 1);
+      const float E = E0 + __shfl_sync(kAll, sum[0] + sum[1], 0);
       const float inv = 1.f / l, Di = E * inv, lse = m + log2f(l);
       if (lane == 0) {
         s_m[rr] = lse;
         s_E[rr] = Di;
         a.stats[row] = make_float2(lse, Di);
       }
-      // lanes tq = 0 hold A, tq = 1 Bk, of dimensions 32 c + 8 (gr / 2) +
-      // gr % 2 + {0, 2, 4, 6}
+      // lanes tq = 0 (2) hold A of the lines' first (second) halves, tq = 1
+      // (3) Bk: dimensions 8 (gr / 2) + gr % 2 + {0, 2, 4, 6} of a half
 #pragma unroll
-      for (int t = 0; t < 2 * NC; ++t)
+      for (int t = 0; t < 2 * NL; ++t)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const float v = acc[t][2 * u] + acc[t][2 * u + 1];
           const float o = __shfl_down_sync(kAll, v, 1);
-          if (tq == 0)
-            s_dq[rr * D + 32 * (t / 2) + 8 * (gr >> 1) + (gr & 1) +
+          if ((tq & 1) == 0)
+            s_dq[rr * D + 64 * (t >> 1) + 16 * tq + 8 * kq + half +
                  4 * (t & 1) + 2 * u] = (v - Di * o) * inv * sc;
         }
       __syncwarp();

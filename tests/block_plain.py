@@ -104,9 +104,9 @@ def attention_backward(Q, K, V, dO, idx):
     the exponentials, the running maximum's rescales and the sum; dP by
     (d + 4) 2 U sum|dO v|; D by the sum of its terms' errors.  dS is taken as
     e dP - D e, so its terms count with |dP| + |D|.  bf16 operands of a
-    matrix product hold p and dS in two parts (2^-16 relative), and an fp32 dO
-    beside bf16 inputs as well (2^-16 in dP; in dV its lo part meets p's hi
-    part only, 2^-16 more).  The sums over rows or keys add (their length + 8)
+    matrix product hold p and dS in two parts (2^-16 relative), and so do the
+    terms of p's normaliser (2^-16 more); an fp32 dO beside bf16 inputs as
+    well (2^-16 in dP; in dV its lo part meets p's hi part only, 2^-16 more).  The sums over rows or keys add (their length + 8)
     2 U of their magnitudes."""
     d, L = Q.shape[-1], K.shape[2]
     B, Hkv = K.shape[:2]
@@ -124,8 +124,8 @@ def attention_backward(Q, K, V, dO, idx):
     D = (P * dP).sum(-1, keepdim=True)
     dS = P * (dP - D) * sc
     C = idx.shape[-1]
-    split = 2.0 ** -16 if Q.dtype == torch.bfloat16 else 0.0
-    planes = split if dO.dtype == torch.float32 else 0.0
+    split = 2.0 ** -15 if Q.dtype == torch.bfloat16 else 0.0
+    planes = split / 2 if dO.dtype == torch.float32 else 0.0
     rp = 2 * eS + (4 * C + 64) * U + split
     edP = (2 * (d + 4) * U + planes) * (Gd.abs() @ T(Vd.abs()))
     eD = (P * (edP + rp * dP.abs())).sum(-1, keepdim=True)
