@@ -26,6 +26,23 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same into fresh sums.
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1,
+                                     uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+      "{%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// 2^x, 0 below the smallest normal number: no term of a sum that holds 2^0
+// (or a probability) misses what is lost there.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // The transpose of an 8 x 8 tile of 16-bit elements held one row per four
 // lanes, two elements per lane.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -83,23 +100,31 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t* hi,
 //      D: dS, and dQ's window part.
 // The window is 5 blocks of 16 x 16 per 16 rows at W = 64, so computing its
 // scores twice costs less than keeping a second accumulator.  What a warp
-// waits for is latency (a gathered row comes from L2): the index rows are
-// read in one batch, and the next V and K rows are asked for as soon as the
-// registers of the current ones are free.
-constexpr int kRowWarps = 4;
+// waits for is latency: a gathered row comes from L2, and a CTA walks through
+// a dozen dependent steps.  So the index rows are read in one batch, the
+// next V and K rows are asked for as soon as the registers of the current
+// ones are free, the window's keys are staged one chunk ahead, and the last
+// phase goes through the chunks backwards, starting with the two that are
+// still there.  Two warps share 16 rows: in the window each takes every
+// second block of keys, in the Top-k eight rows.
+constexpr int kRowWarps = 8;
+constexpr int kWarpRows = 64 / kRowWarps;  // Top-k rows of a warp
 
 template <int D, int NP>
 struct RowSmem {
-  static constexpr int CK = 64;         // keys staged at a time
+  static constexpr int CK = 64;         // keys of a chunk
   static constexpr int RS = D * 2 + 16; // padded row (bytes)
-  // K and V of the window, or q and dO of the CTA's rows
-  static constexpr size_t stage = (size_t)(NP + 1) * 64 * RS;
-  __host__ __device__ static size_t per_warp(int kk) {
-    return (size_t)16 * D * 4 + 4 * 16 * 4 + (size_t)kk * 8 +
-           (size_t)16 * kk * 4;
-  }
-  static size_t bytes(int k) {
-    return stage + kRowWarps * per_warp((k + 15) / 16 * 16);
+  static constexpr size_t rows = (size_t)(NP + 1) * 64 * RS;   // q, dO
+  static constexpr size_t chunk = (size_t)2 * CK * RS;         // K, V
+  static constexpr size_t anchor = (size_t)2 * 16 * RS;        // K, V
+  static constexpr int DS = D + 8;  // dQ row: no two of 8 rows on a bank
+  static constexpr size_t dq = (size_t)64 * DS * 4;
+  static constexpr size_t stat = (size_t)64 * 4;  // one number per row
+  __host__ __device__ static size_t bytes(int k) {
+    const size_t kk = (k + 15) / 16 * 16;
+    // 2 x 3 running sums, the log-sum-exp, D, the Top-k count
+    return rows + 2 * chunk + anchor + dq + 9 * stat +
+           kRowWarps * kk * 8 + 64 * kk * 4;
   }
 };
 
@@ -125,41 +150,51 @@ struct Gather {
       }
     }
   }
-  // Products of all rows with a vector whose halves of each line stand in
-  // the even and odd columns of B (w: this lane's 16 bytes of a line).  The
-  // result for key 4 tq + gr / 2.
-  __device__ __forceinline__ float dot(const uint4 (&w)[NL], int gr,
-                                       int tq) const {
-    float d[2][4];
-    add_dot(w, d, true);
-    return pick(d, gr, tq);
-  }
-  __device__ __forceinline__ void add_dot(const uint4 (&w)[NL],
-                                          float (&d)[2][4], bool clear) const {
+  // One product per load, its registers as they are: row gr of A is key
+  // gr / 2, half gr % 2 of the line, elements {0, 1, 4, 5} of each 16 bytes,
+  // row gr + 8 the same with {2, 3, 6, 7}.  Column n of B is the vector's
+  // part for (half (n / 2) % 2, elements by n % 2), so the sums that belong
+  // together are c0 and c3 of the lanes with gr % 2 == tq % 2, and those of
+  // the lane across both bits.
+  __device__ __forceinline__ void add_dot(const uint32_t (&w)[NL][2],
+                                          float (&d)[4][4],
+                                          bool clear) const {
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      if (clear) d[g][0] = d[g][1] = d[g][2] = d[g][3] = 0.f;
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
       for (int c = 0; c < NL; ++c) {
-        mma(d[g], v[2 * g][c][0], v[2 * g + 1][c][0], v[2 * g][c][1],
-            v[2 * g + 1][c][1], w[c].x, w[c].y);
-        mma(d[g], v[2 * g][c][2], v[2 * g + 1][c][2], v[2 * g][c][3],
-            v[2 * g + 1][c][3], w[c].z, w[c].w);
+        if (clear && c == 0)
+          mma0(d[i], v[i][c][0], v[i][c][1], v[i][c][2], v[i][c][3], w[c][0],
+               w[c][1]);
+        else
+          mma(d[i], v[i][c][0], v[i][c][1], v[i][c][2], v[i][c][3], w[c][0],
+              w[c][1]);
       }
     }
   }
-  // Row gr (and gr + 8) of a product is key gr / 2 of a load, its first half
-  // at even gr (even columns), its second at odd gr (odd columns).
-  __device__ __forceinline__ static float pick(const float (&d)[2][4], int gr,
+  // In a lane with gr % 2 == tq % 2: the product of key gr / 2 of load tq.
+  __device__ __forceinline__ static float pick(const float (&d)[4][4], int gr,
                                                int tq) {
-    const bool odd = gr & 1;
-    const float a0 = odd ? d[0][1] : d[0][0], a1 = odd ? d[0][3] : d[0][2];
-    const float b0 = odd ? d[1][1] : d[1][0], b1 = odd ? d[1][3] : d[1][2];
-    const float a = (tq & 1) ? a1 : a0, b = (tq & 1) ? b1 : b0;
-    const float x = (tq & 2) ? b : a;
-    return x + __shfl_xor_sync(kAll, x, 4);
+    const float p0 = d[0][0] + d[0][3], p1 = d[1][0] + d[1][3];
+    const float p2 = d[2][0] + d[2][3], p3 = d[3][0] + d[3][3];
+    const float a = (tq & 2) ? p2 : p0, b = (tq & 2) ? p3 : p1;
+    const float keep = (gr & 1) ? b : a, send = (gr & 1) ? a : b;
+    return keep + __shfl_xor_sync(kAll, send, 5);
   }
 };
+
+// B operand of add_dot from a row in shared memory.
+template <int NL>
+__device__ __forceinline__ void dot_operand(const unsigned char* row, int gr,
+                                            int tq, uint32_t (&w)[NL][2]) {
+#pragma unroll
+  for (int c = 0; c < NL; ++c) {
+    const uint4 t = *reinterpret_cast<const uint4*>(
+        row + 128 * c + 64 * ((gr >> 1) & 1) + 16 * tq);
+    w[c][0] = (gr & 1) ? t.y : t.x;
+    w[c][1] = (gr & 1) ? t.w : t.z;
+  }
+}
 
 // The largest of the warp's values.
 __device__ __forceinline__ float warp_max(float x) {
@@ -169,85 +204,107 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 template <int D, int NP>
-__global__ void __launch_bounds__(kRowWarps * 32, D == 64 ? 4 : 2)
+__global__ void __launch_bounds__(kRowWarps * 32, D == 64 ? 2 : 1)
 backward_rows_mma(Args a, int ntile) {
   using SM = RowSmem<D, NP>;
-  constexpr int RS = SM::RS, CK = SM::CK;
+  constexpr int RS = SM::RS, CK = SM::CK, DS = SM::DS;
   constexpr int KS = D / 16;  // steps of a product over the head dimension
   constexpr int NT = D / 8;   // its 8-wide tiles
   extern __shared__ __align__(16) unsigned char g_smem[];
-  __shared__ int s_kmin, s_any;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int gr = lane >> 2, tq = lane & 3;
+  const int rg = wid & 3, hf = wid >> 2;  // row group, which half of its work
   const int k = a.k, kk = (k + 15) / 16 * 16;
   const int nq = a.nq, L = a.L;
   const int bh = blockIdx.x / ntile;
   const int r0 = (blockIdx.x % ntile) * 64;
   const int b = bh / a.Hq, h = bh % a.Hq;
   const int seg = b * a.Hkv + h / (a.Hq / a.Hkv);
-  const int i0 = r0 + wid * 16;  // the warp's first row
   const int64_t rowbase = (int64_t)bh * nq;
   const bf* Qg = reinterpret_cast<const bf*>(a.Q) + rowbase * D;
   const bf* Kg = reinterpret_cast<const bf*>(a.K) + (int64_t)seg * L * D;
   const bf* Vg = reinterpret_cast<const bf*>(a.V) + (int64_t)seg * L * D;
-  unsigned char* sK = g_smem;
-  unsigned char* sV = g_smem + (size_t)CK * RS;
-  float* s_dq = reinterpret_cast<float*>(g_smem + SM::stage +
-                                         (size_t)wid * SM::per_warp(kk));
-  float* s_m = s_dq + 16 * D;  // running maximum, then the log-sum-exp
-  float* s_l = s_m + 16;
-  float* s_E = s_l + 16;       // sum e dP, then D
-  int* s_top = reinterpret_cast<int*>(s_E + 16);  // Top-k entries of a row
-  float2* s_xd = reinterpret_cast<float2*>(s_top + 16);  // one row's (x, dP)
-  int* s_idx = reinterpret_cast<int*>(s_xd + kk);
+  unsigned char* sR = g_smem;              // q and dO
+  unsigned char* sC = sR + SM::rows;       // two chunks of K and V
+  unsigned char* sA = sC + 2 * SM::chunk;  // the first 16 keys
+  float* s_dq = reinterpret_cast<float*>(sA + SM::anchor);
+  float* s_part = s_dq + 64 * DS;  // [half][m, l, E][row]
+  float* s_lse = s_part + 6 * 64;
+  float* s_D = s_lse + 64;
+  int* s_top = reinterpret_cast<int*>(s_D + 64);  // Top-k entries of a row
+  float2* s_xd = reinterpret_cast<float2*>(s_top + 64) + wid * kk;
+  int* s_idx = reinterpret_cast<int*>(
+      reinterpret_cast<float2*>(s_top + 64) + kRowWarps * kk);
   const float sl2 = kLog2e / sqrtf((float)D), sc = 1.f / sqrtf((float)D);
   constexpr int kPieces = D * 2 / 16;  // 16-byte pieces of a row
 
-  // q and the planes of dO, rows r0 .. r0 + 63, where K and V are staged in
-  // the other phases
-  auto stage_rows = [&]() {
-    for (int e = threadIdx.x; e < 64 * kPieces; e += kRowWarps * 32) {
-      const int rr = e / kPieces, pc = e % kPieces;
-      const int64_t at = (int64_t)min(r0 + rr, nq - 1) * D + pc * 8;
-      unsigned char* dst = g_smem + rr * RS + pc * 16;
-      cp_async16(dst, Qg + at);
+  // the keys that the CTA's rows see: every warp looks at all 64 rows
+  int kmin_c = 0x7FFFFFFF;
 #pragma unroll
-      for (int p = 0; p < NP; ++p)
-        cp_async16(dst + (size_t)(p + 1) * 64 * RS, a.g[p] + rowbase * D + at);
+  for (int u = 0; u < 2; ++u) {
+    int w;
+    kmin_c = min(kmin_c, window_lo(a, b, h, min(r0 + 32 * u + lane, nq - 1),
+                                   false, &w));
+  }
+  kmin_c = __reduce_min_sync(kAll, kmin_c);
+  const int cs0 = kmin_c & ~15;
+  const int kmax_c = a.p0 + min(r0 + 63, nq - 1);
+  const int nch = (kmax_c - cs0) / CK + 1;
+  auto copy_keys = [&](unsigned char* dst, int first, int count, int stride) {
+    for (int e = threadIdx.x; e < count * kPieces; e += kRowWarps * 32) {
+      const int rr = e / kPieces, pc = e % kPieces;
+      const int j = min(first + rr, L - 1);  // rows past the cache: any valid
+      cp_async16(dst + rr * RS + pc * 16, Kg + (size_t)j * D + pc * 8);
+      cp_async16(dst + (stride + rr) * RS + pc * 16,
+                 Vg + (size_t)j * D + pc * 8);
     }
   };
-  stage_rows();
-  if (threadIdx.x == 0) {
-    s_kmin = 0x7FFFFFFF;
-    s_any = 0;
+  auto stage = [&](int ch) {  // chunk ch, in a group of its own
+    if (ch >= 0 && ch < nch)
+      copy_keys(sC + (ch & 1) * SM::chunk, cs0 + ch * CK,
+                min(CK, (kmax_c + 1 - cs0 - ch * CK + 15) & ~15), CK);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int e = threadIdx.x; e < 64 * kPieces; e += kRowWarps * 32) {
+    const int rr = e / kPieces, pc = e % kPieces;
+    const int64_t at = (int64_t)min(r0 + rr, nq - 1) * D + pc * 8;
+    unsigned char* dst = sR + rr * RS + pc * 16;
+    cp_async16(dst, Qg + at);
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+      cp_async16(dst + (size_t)(p + 1) * 64 * RS, a.g[p] + rowbase * D + at);
   }
+  copy_keys(sA, 0, 16, 16);
+  stage(0);
+  stage(1);
 
-  // the windows and Top-k counts of the warp's rows, a row per lane, and the
-  // Top-k positions: checked, kept, and written as the entries' sort keys
-  const int nrow = min(16, nq - i0);  // 0 or less: no rows
+  // the windows and Top-k counts of the warp's Top-k rows, a row per lane,
+  // and their Top-k positions: checked, kept, and written as sort keys
+  const int t_row = rg * 16 + hf * kWarpRows;  // first of them in the tile
+  const int nrow = min(kWarpRows, nq - r0 - t_row);  // 0 or less: none
   {
-    const int rr = min(lane, max(nrow, 1) - 1);
-    const int r = min(i0 + rr, nq - 1);
     const bool mine = lane < nrow;
+    const int r = min(r0 + t_row + min(lane, kWarpRows - 1), nq - 1);
     int w;
     const int lo = window_lo(a, b, h, r, mine, &w);
     const int m = listed_count(a, rowbase + r, a.p0 + r, lo, w, mine);
-    if (mine) s_top[lane] = m;
+    if (mine) s_top[t_row + lane] = m;
     const int last = a.p0 + r - w;  // the last candidate
-    uint32_t* key = a.key[0] + (rowbase + i0) * (k + 1);
+    const int64_t first = rowbase + r0 + t_row;
+    uint32_t* key = a.key[0] + first * (k + 1);
     if (mine) key[(int64_t)lane * (k + 1)] = lo > 0 ? 0u : (uint32_t)L;
-    const int32_t* ix = a.idx + (rowbase + i0) * a.C_max + 1;
+    const int32_t* ix = a.idx + first * a.C_max + 1;
 #pragma unroll 1
     for (int t0 = 0; t0 < k; t0 += 32) {
       const int t = t0 + lane;
-      int j[16];
+      int j[kWarpRows];
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
+      for (int u = 0; u < kWarpRows; ++u) {
         const int mu = __shfl_sync(kAll, m, u);
         j[u] = u < nrow && t < mu ? __ldg(ix + (int64_t)u * a.C_max + t) : -1;
       }
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
+      for (int u = 0; u < kWarpRows; ++u) {
         const int mu = __shfl_sync(kAll, m, u);
         const int lu = __shfl_sync(kAll, last, u);
         if (u < nrow && t < k) {
@@ -256,17 +313,16 @@ backward_rows_mma(Args a, int ntile) {
             raise_flag(a.status, kErrCmax);
             v = -1;
           }
-          s_idx[u * kk + t] = v;
+          s_idx[(t_row + u) * kk + t] = v;
           key[(int64_t)u * (k + 1) + 1 + t] = v < 0 ? (uint32_t)L : (uint32_t)v;
         }
       }
     }
   }
-  cp_async_wait_all();
-  __syncthreads();
 
-  // this lane's two rows of the warp's 16 in the window products
-  const bool wlive = nrow > 0;
+  // this lane's two rows of the 16 that its warp has in the window products
+  const int i0 = r0 + rg * 16;
+  const bool wlive = i0 < nq;
   const int ra = i0 + gr, rb = ra + 8;
   const bool va = ra < nq, vb = rb < nq;
   const int ca = min(ra, nq - 1), cb = min(rb, nq - 1);
@@ -274,21 +330,21 @@ backward_rows_mma(Args a, int ntile) {
   int wa, wb;
   const int loa = window_lo(a, b, h, ca, false, &wa);
   const int lob = window_lo(a, b, h, cb, false, &wb);
-  int kmin = min(loa, lob);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-    kmin = min(kmin, __shfl_xor_sync(kAll, kmin, off));
+  const int kmin = __reduce_min_sync(kAll, min(loa, lob));
   const int kmax = a.p0 + min(i0 + 15, nq - 1);
-  const bool anchors = __any_sync(kAll, (va && loa > 0) || (vb && lob > 0));
-  if (wlive && lane == 0) {
-    atomicMin(&s_kmin, kmin);
-    if (anchors) s_any = 1;
-  }
+  // keys that all of the warp's 16 rows see
+  const int inner_lo = __reduce_max_sync(kAll, max(loa, lob));
+  const int inner_hi = i0 + 15 < nq ? a.p0 + i0 : -1;
+  // the anchor's block falls to the first warp of the pair
+  const bool anchors =
+      __any_sync(kAll, (va && loa > 0) || (vb && lob > 0)) && hf == 0 && wlive;
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+  __syncthreads();
   // A operands of the window products: q and dO of the warp's rows
   uint32_t qa[KS][4], ga[NP][KS][4];
   auto fragments = [&]() {
     const unsigned char* at =
-        g_smem + (wid * 16 + (lane & 15)) * RS + (lane >> 4) * 16;
+        sR + (rg * 16 + (lane & 15)) * RS + (lane >> 4) * 16;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       ldsm4(qa[ks], at + ks * 32);
@@ -298,52 +354,40 @@ backward_rows_mma(Args a, int ntile) {
     }
   };
   fragments();
-  __syncthreads();
-  const int cs0 = s_kmin & ~15;
-  const int kmax_c = a.p0 + min(r0 + 63, nq - 1);
-  const int nch = (kmax_c - cs0) / CK + 1;
-  const int m0 = s_any ? -1 : 0;  // chunk -1: the anchor's 16 keys
-
-  auto stage = [&](int m) {
-    const int cs = m < 0 ? 0 : cs0 + m * CK;
-    const int rows = m < 0 ? 16 : min(CK, kmax_c + 1 - cs);
-    for (int e = threadIdx.x; e < ((rows + 15) & ~15) * kPieces;
-         e += kRowWarps * 32) {
-      const int rr = e / kPieces, pc = e % kPieces;
-      const int j = min(cs + rr, L - 1);  // rows past the cache: any valid
-      cp_async16(sK + rr * RS + pc * 16, Kg + (size_t)j * D + pc * 8);
-      cp_async16(sV + rr * RS + pc * 16, Vg + (size_t)j * D + pc * 8);
-    }
-    cp_async_wait_all();
-  };
   // scores (log2 units, masked to -inf) and dP of the 16 x 16 block of keys
   // kb.. (at place kl of the staged chunk), as two accumulators of 8 keys
-  auto block = [&](int kb, int kl, bool anchor, float (&x)[2][4],
-                   float (&dp)[2][4]) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) x[t][c] = dp[t][c] = 0.f;
-    const int lr = kl + (lane & 7) + ((lane >> 4) << 3);
-    const int lc = ((lane >> 3) & 1) * 16;
+  auto block = [&](const unsigned char* sk, int stride, int kb, bool anchor,
+                   float (&x)[2][4], float (&dp)[2][4]) {
+    const unsigned char* at = sk + ((lane & 7) + ((lane >> 4) << 3)) * RS +
+                              ((lane >> 3) & 1) * 16;
+    auto step = [&](float (&d)[4], const uint32_t (&A)[4], uint32_t b0,
+                    uint32_t b1, bool first) {
+      if (first) mma0(d, A[0], A[1], A[2], A[3], b0, b1);
+      else mma(d, A[0], A[1], A[2], A[3], b0, b1);
+    };
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       uint32_t f[4];
-      ldsm4(f, sK + lr * RS + ks * 32 + lc);
-      mma(x[0], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], f[0], f[1]);
-      mma(x[1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], f[2], f[3]);
+      ldsm4(f, at + ks * 32);
+      step(x[0], qa[ks], f[0], f[1], ks == 0);
+      step(x[1], qa[ks], f[2], f[3], ks == 0);
     }
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       uint32_t f[4];
-      ldsm4(f, sV + lr * RS + ks * 32 + lc);
+      ldsm4(f, at + stride * RS + ks * 32);
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        mma(dp[0], ga[p][ks][0], ga[p][ks][1], ga[p][ks][2], ga[p][ks][3],
-            f[0], f[1]);
-        mma(dp[1], ga[p][ks][0], ga[p][ks][1], ga[p][ks][2], ga[p][ks][3],
-            f[2], f[3]);
+        step(dp[0], ga[p][ks], f[0], f[1], ks == 0 && p == 0);
+        step(dp[1], ga[p][ks], f[2], f[3], ks == 0 && p == 0);
       }
+    }
+    if (!anchor && kb >= inner_lo && kb + 15 <= inner_hi) {  // seen by all
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[t][c] *= sl2;
+      return;
     }
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -356,63 +400,76 @@ backward_rows_mma(Args a, int ntile) {
         x[t][c] = ok ? x[t][c] * sl2 : -INFINITY;
       }
   };
+  // this warp's first block of keys in the chunk that begins at cs
+  auto first_block = [&](int cs) {
+    const int kb = max(cs, kmin & ~15);
+    return kb + (((kb >> 4) ^ hf) & 1) * 16;
+  };
 
   // ---- 1: window and anchor, running sums
   {
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, E[2] = {0.f, 0.f};
-#pragma unroll 1
-    for (int ch = m0; ch < nch; ++ch) {
-      stage(ch);
-      __syncthreads();
-      const int cs = ch < 0 ? 0 : cs0 + ch * CK;
-      const int jlo = ch < 0 ? 0 : max(cs, kmin & ~15);
-      const int jhi = ch < 0 ? (anchors ? 0 : -1) : min(cs + CK - 1, kmax);
-#pragma unroll 1
-      for (int kb = jlo; wlive && kb <= jhi; kb += 16) {
-        float x[2][4], dp[2][4];
-        block(kb, kb - cs, ch < 0, x, dp);
+    auto add = [&](const float (&x)[2][4], const float (&dp)[2][4]) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float mx = fmaxf(fmaxf(x[0][2 * u], x[0][2 * u + 1]),
-                                 fmaxf(x[1][2 * u], x[1][2 * u + 1]));
-          if (mx > m[u]) {
-            const float f = exp2f(m[u] - mx);
-            l[u] *= f;
-            E[u] *= f;
-            m[u] = mx;
-          }
-          if (m[u] == -INFINITY) continue;
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const float e = exp2f(x[t][2 * u + c] - m[u]);
-              l[u] += e;
-              E[u] = fmaf(e, dp[t][2 * u + c], E[u]);
-            }
+      for (int u = 0; u < 2; ++u) {
+        const float mx = fmaxf(fmaxf(x[0][2 * u], x[0][2 * u + 1]),
+                               fmaxf(x[1][2 * u], x[1][2 * u + 1]));
+        if (mx > m[u]) {
+          const float f = ex2(m[u] - mx);
+          l[u] *= f;
+          E[u] *= f;
+          m[u] = mx;
         }
+        if (m[u] == -INFINITY) continue;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float e = ex2(x[t][2 * u + c] - m[u]);
+            l[u] += e;
+            E[u] = fmaf(e, dp[t][2 * u + c], E[u]);
+          }
       }
-      __syncthreads();
+    };
+    if (anchors) {
+      float x[2][4], dp[2][4];
+      block(sA, 16, 0, true, x, dp);
+      add(x, dp);
     }
-    stage_rows();  // for the Top-k and the last phase
+#pragma unroll 1
+    for (int ch = 0; ch < nch; ++ch) {
+      if (ch > 0) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // chunk ch is there, chunk ch - 1 has been read
+        if (ch + 1 < nch) stage(ch + 1);
+      }
+      const int cs = cs0 + ch * CK;
+#pragma unroll 1
+      for (int kb = first_block(cs); wlive && kb <= min(cs + CK - 1, kmax);
+           kb += 32) {
+        float x[2][4], dp[2][4];
+        block(sC + (ch & 1) * SM::chunk + (kb - cs) * RS, CK, kb, false, x, dp);
+        add(x, dp);
+      }
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       float mx = m[u];
       mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
-      const float f = m[u] == -INFINITY ? 0.f : exp2f(m[u] - mx);
+      const float f = m[u] == -INFINITY ? 0.f : ex2(m[u] - mx);
       float ll = l[u] * f, EE = E[u] * f;
       ll += __shfl_xor_sync(kAll, ll, 1);
       EE += __shfl_xor_sync(kAll, EE, 1);
       ll += __shfl_xor_sync(kAll, ll, 2);
       EE += __shfl_xor_sync(kAll, EE, 2);
       if (tq == 0) {
-        s_m[gr + 8 * u] = mx;
-        s_l[gr + 8 * u] = ll;
-        s_E[gr + 8 * u] = EE;
+        float* p = s_part + hf * 3 * 64 + rg * 16 + gr + 8 * u;
+        p[0] = mx;
+        p[64] = ll;
+        p[128] = EE;
       }
     }
-    cp_async_wait_all();
     __syncthreads();
   }
 
@@ -422,27 +479,49 @@ backward_rows_mma(Args a, int ntile) {
     const bf* Kl = Kg + 8 * (lane & 7);
     const bf* Vl = Vg + 8 * (lane & 7);
     const int half = gr & 1, kq = gr >> 1;
+    const bool owner = half == (tq & 1);  // this lane's key: see pick
+    const int key = 4 * (owner ? tq : tq ^ 1) + kq;
+    // places of the weights' bf16 parts in B: low halves for the rows' first
+    // halves (columns 0-3), high halves for the second
+    const uint32_t sel0 = gr >= 4 ? 0x1044u : 0x4410u;
+    const uint32_t sel1 = gr >= 4 ? 0x3244u : 0x4432u;
+    const uint32_t ones = 0x3F803F80u;  // two bf16 ones
+    // the running sums of both warps of a pair, a row per lane
+    float pm = 0.f, pl = 0.f, pE = 0.f;
+    if (lane < nrow) {
+      const float* p = s_part + t_row + lane;
+      const float m1 = p[0], m2 = p[3 * 64];
+      pm = fmaxf(m1, m2);
+      const float f1 = ex2(m1 - pm), f2 = ex2(m2 - pm);
+      pl = p[64] * f1 + p[4 * 64] * f2;
+      pE = p[128] * f1 + p[5 * 64] * f2;
+    }
     Gather<D> kr, vr;
     int j[4];  // the entries in kr and vr (-1: none, row 0 is read)
     auto entries = [&](int rr, int g0) {
-      const int mt = s_top[rr];
-      const int* ix = s_idx + rr * kk + g0 + kq;
+      const int mt = s_top[t_row + rr] - g0 - kq;
+      const int* ix = s_idx + (t_row + rr) * kk + g0 + kq;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) j[i] = g0 + 4 * i + kq < mt ? ix[4 * i] : -1;
+      for (int i = 0; i < 4; ++i) j[i] = 4 * i < mt ? ix[4 * i] : -1;
     };
-    if (wlive && s_top[0] > 0) {
+    if (nrow > 0 && s_top[t_row] > 0) {
       entries(0, 0);
       kr.load(Kl, j);
       vr.load(Vl, j);
     }
 #pragma unroll 1
     for (int rr = 0; rr < nrow; ++rr) {
-      const int64_t row = rowbase + i0 + rr;
-      const int mt = s_top[rr];
-      float m = s_m[rr], l0 = s_l[rr], E0 = s_E[rr];  // window and anchor
-      // even columns: first halves of the lines, odd columns: second halves
-      const unsigned char* qrow =
-          g_smem + (wid * 16 + rr) * RS + 64 * half + 16 * tq;
+      const int tr = t_row + rr;  // in the tile
+      const int64_t row = rowbase + r0 + tr;
+      const int mt = s_top[tr];
+      float m = __shfl_sync(kAll, pm, rr), l = __shfl_sync(kAll, pl, rr);
+      float E = __shfl_sync(kAll, pE, rr);
+      uint32_t wq[NL][2], wg[NP][NL][2];
+      dot_operand<NL>(sR + tr * RS, gr, tq, wq);
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        dot_operand<NL>(sR + (size_t)(p + 1) * 64 * RS + tr * RS, gr, tq,
+                        wg[p]);
       // sums: acc of the rows' dimensions, sum of the weights alone (columns
       // 0, 1: e dP, columns 2, 3: e)
       float acc[2 * NL][4], sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -450,45 +529,33 @@ backward_rows_mma(Args a, int ntile) {
       for (int t = 0; t < 2 * NL; ++t)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[t][c] = 0.f;
-      if (mt == 0 && rr + 1 < nrow && s_top[rr + 1] > 0) {
+      if (mt == 0 && rr + 1 < nrow && s_top[tr + 1] > 0) {
         entries(rr + 1, 0);  // nothing was read ahead
         kr.load(Kl, j);
         vr.load(Vl, j);
       }
 #pragma unroll 1
       for (int g0 = 0; g0 < mt; g0 += 16) {
-        // this lane's key of the softmax: 4 tq + gr / 2
-        const int mine = g0 + 4 * tq + kq;
-        const bool use = mine < mt && s_idx[rr * kk + mine] >= 0;
+        const bool use = g0 + key < mt && s_idx[tr * kk + g0 + key] >= 0;
         // the next entries: of this row, or the first of the next one
         const bool same = g0 + 16 < mt;
         entries(same ? rr : min(rr + 1, nrow - 1), same ? g0 + 16 : 0);
-        float d[2][4];
+        float d[4][4];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          uint4 w[NL];
-#pragma unroll
-          for (int c = 0; c < NL; ++c)
-            w[c] = *reinterpret_cast<const uint4*>(
-                qrow + (size_t)(p + 1) * 64 * RS + 128 * c);
-          vr.add_dot(w, d, p == 0);
-        }
+        for (int p = 0; p < NP; ++p) vr.add_dot(wg[p], d, p == 0);
         vr.load(Vl, j);
         const float dp = Gather<D>::pick(d, gr, tq);
-        float x;
-        {
-          uint4 w[NL];
-#pragma unroll
-          for (int c = 0; c < NL; ++c)
-            w[c] = *reinterpret_cast<const uint4*>(qrow + 128 * c);
-          x = kr.dot(w, gr, tq);
-        }
-        x = use ? x * sl2 : -INFINITY;
+        kr.add_dot(wq, d, true);
+        float x = Gather<D>::pick(d, gr, tq);
+        // the neighbour without a key of its own takes this one's score, to
+        // hand out e where this lane hands out e dP
+        const float y = __shfl_xor_sync(kAll, x, 1);
+        x = use ? (owner ? x : y) * sl2 : -INFINITY;
         const float mx = warp_max(x);
         if (mx > m) {  // the same for the whole warp
-          const float f = exp2f(m - mx);
-          l0 *= f;
-          E0 *= f;
+          const float f = ex2(m - mx);
+          l *= f;
+          E *= f;
 #pragma unroll
           for (int c = 0; c < 4; ++c) sum[c] *= f;
 #pragma unroll
@@ -497,24 +564,27 @@ backward_rows_mma(Args a, int ntile) {
             for (int c = 0; c < 4; ++c) acc[t][c] *= f;
           m = mx;
         }
-        const float e = exp2f(x - m);
-        if (half == 0) s_xd[mine] = make_float2(x, dp);
+        const float e = ex2(x - m);
+        if (owner) s_xd[g0 + key] = make_float2(x, dp);
         // B: columns 0-3 (4-7) weigh the rows' first (second) halves with
         // e dP (hi, lo) and e (hi, lo); its row pair (2 tq, 2 tq + 1) is the
         // two halves of key tq of a load
-        const float w = half ? e : e * dp;
-        const int src = 8 * tq + 4 * ((gr >> 1) & 1);
+        const float w = owner ? e * dp : e;
         uint32_t B[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = __shfl_sync(kAll, w, src + i);
-          const uint32_t hi = pack2(v, 0.f);
-          const uint32_t t = half ? pack2(v - bf16lo(hi), 0.f) : hi;
-          B[i] = gr >= 4 ? t << 16 : t;
+        for (int i = 0; i < 4; i += 2) {
+          const int src = 8 * tq + i;
+          const int sx = (gr >> 1) & 1;
+          const float v0 = __shfl_sync(kAll, w, src ^ sx);
+          const float v1 = __shfl_sync(kAll, w, (src + 5) ^ sx);
+          uint32_t hi, lo;
+          split2(v0, v1, &hi, &lo);
+          const uint32_t t = half ? lo : hi;
+          B[i] = __byte_perm(t, 0u, sel0);
+          B[i + 1] = __byte_perm(t, 0u, sel1);
         }
-        constexpr uint32_t kOnes = 0x3F803F80u;  // two bf16 ones
-        mma(sum, kOnes, kOnes, kOnes, kOnes, B[0], B[1]);
-        mma(sum, kOnes, kOnes, kOnes, kOnes, B[2], B[3]);
+        mma(sum, ones, ones, ones, ones, B[0], B[1]);
+        mma(sum, ones, ones, ones, ones, B[2], B[3]);
 #pragma unroll
         for (int c = 0; c < NL; ++c)
 #pragma unroll
@@ -528,12 +598,12 @@ backward_rows_mma(Args a, int ntile) {
                   B[2 * g + 1]);
         kr.load(Kl, j);
       }
-      const float l = l0 + __shfl_sync(kAll, sum[0] + sum[1], 1);
-      const float E = E0 + __shfl_sync(kAll, sum[0] + sum[1], 0);
+      l += __shfl_sync(kAll, sum[0] + sum[1], 1);
+      E += __shfl_sync(kAll, sum[0] + sum[1], 0);
       const float inv = 1.f / l, Di = E * inv, lse = m + log2f(l);
       if (lane == 0) {
-        s_m[rr] = lse;
-        s_E[rr] = Di;
+        s_lse[tr] = lse;
+        s_D[tr] = Di;
         a.stats[row] = make_float2(lse, Di);
       }
       // lanes tq = 0 (2) hold A of the lines' first (second) halves, tq = 1
@@ -545,7 +615,7 @@ backward_rows_mma(Args a, int ntile) {
           const float v = acc[t][2 * u] + acc[t][2 * u + 1];
           const float o = __shfl_down_sync(kAll, v, 1);
           if ((tq & 1) == 0)
-            s_dq[rr * D + 64 * (t >> 1) + 16 * tq + 8 * kq + half +
+            s_dq[tr * DS + 64 * (t >> 1) + 16 * tq + 8 * kq + half +
                  4 * (t & 1) + 2 * u] = (v - Di * o) * inv * sc;
         }
       __syncwarp();
@@ -554,7 +624,7 @@ backward_rows_mma(Args a, int ntile) {
         float2 o = make_float2(0.f, 0.f);
         if (t < mt) {
           const float2 xd = s_xd[t];
-          o.x = exp2f(xd.x - lse);  // 0 where the slot was refused
+          o.x = ex2(xd.x - lse);  // 0 where the slot was refused
           o.y = o.x * (xd.y - Di) * sc;
         }
         pds[1 + t] = o;
@@ -564,72 +634,84 @@ backward_rows_mma(Args a, int ntile) {
   }
 
   // ---- 3: dS of the window and the anchor
+  __syncthreads();
+  float o[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[t][c] = 0.f;
   {
     fragments();
-    __syncthreads();
-    float o[NT][4];
+    const int sr = rg * 16 + gr;
+    const float lse[2] = {s_lse[sr], s_lse[sr + 8]};
+    const float Di[2] = {s_D[sr], s_D[sr + 8]};
+    auto add = [&](const unsigned char* sk, int stride, int kb, bool anchor) {
+      float x[2][4], dp[2][4];
+      block(sk, stride, kb, anchor, x, dp);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[t][c] = 0.f;
-    const float lse[2] = {s_m[gr], s_m[gr + 8]}, Di[2] = {s_E[gr], s_E[gr + 8]};
-#pragma unroll 1
-    for (int ch = m0; ch < nch; ++ch) {
-      stage(ch);
-      __syncthreads();
-      const int cs = ch < 0 ? 0 : cs0 + ch * CK;
-      const int jlo = ch < 0 ? 0 : max(cs, kmin & ~15);
-      const int jhi = ch < 0 ? (anchors ? 0 : -1) : min(cs + CK - 1, kmax);
-#pragma unroll 1
-      for (int kb = jlo; wlive && kb <= jhi; kb += 16) {
-        float x[2][4], dp[2][4];
-        block(kb, kb - cs, ch < 0, x, dp);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float p = exp2f(x[t][c] - lse[c >> 1]);
-            const float ds = p * (dp[t][c] - Di[c >> 1]) * sc;
-            if (ch < 0 && t == 0 && (c & 1) == 0 && tq == 0 &&
-                (c ? vb : va))  // the anchor's entry (zeros without one)
-              a.pds[(rowbase + (c ? rb : ra)) * (k + 1)] = make_float2(p, ds);
-            x[t][c] = ds;
-          }
-        uint32_t hi[4], lo[4];
-        split2(x[0][0], x[0][1], &hi[0], &lo[0]);
-        split2(x[0][2], x[0][3], &hi[1], &lo[1]);
-        split2(x[1][0], x[1][1], &hi[2], &lo[2]);
-        split2(x[1][2], x[1][3], &hi[3], &lo[3]);
-        const unsigned char* kp = sK + (kb - cs + (lane & 15)) * RS +
-                                  (lane >> 4) * 16;
-#pragma unroll
-        for (int t = 0; t < NT; t += 2) {
-          uint32_t f[4];
-          ldsm4t(f, kp + t * 16);
-          mma(o[t], hi[0], hi[1], hi[2], hi[3], f[0], f[1]);
-          mma(o[t], lo[0], lo[1], lo[2], lo[3], f[0], f[1]);
-          mma(o[t + 1], hi[0], hi[1], hi[2], hi[3], f[2], f[3]);
-          mma(o[t + 1], lo[0], lo[1], lo[2], lo[3], f[2], f[3]);
+        for (int c = 0; c < 4; ++c) {
+          const float p = ex2(x[t][c] - lse[c >> 1]);
+          const float ds = p * (dp[t][c] - Di[c >> 1]) * sc;
+          if (anchor && t == 0 && (c & 1) == 0 && tq == 0 && (c ? vb : va))
+            // the anchor's entry (zeros for a row without one)
+            a.pds[(rowbase + (c ? rb : ra)) * (k + 1)] = make_float2(p, ds);
+          x[t][c] = ds;
         }
-      }
-      __syncthreads();
-    }
-    if (!wlive) return;
+      uint32_t hi[4], lo[4];
+      split2(x[0][0], x[0][1], &hi[0], &lo[0]);
+      split2(x[0][2], x[0][3], &hi[1], &lo[1]);
+      split2(x[1][0], x[1][1], &hi[2], &lo[2]);
+      split2(x[1][2], x[1][3], &hi[3], &lo[3]);
+      const unsigned char* kp = sk + (lane & 15) * RS + (lane >> 4) * 16;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float* pa = s_dq + gr * D + 8 * t + 2 * tq;
-      float* pb = pa + 8 * D;
-      pa[0] += o[t][0];
-      pa[1] += o[t][1];
-      pb[0] += o[t][2];
-      pb[1] += o[t][3];
+      for (int t = 0; t < NT; t += 2) {
+        uint32_t f[4];
+        ldsm4t(f, kp + t * 16);
+        mma(o[t], hi[0], hi[1], hi[2], hi[3], f[0], f[1]);
+        mma(o[t], lo[0], lo[1], lo[2], lo[3], f[0], f[1]);
+        mma(o[t + 1], hi[0], hi[1], hi[2], hi[3], f[2], f[3]);
+        mma(o[t + 1], lo[0], lo[1], lo[2], lo[3], f[2], f[3]);
+      }
+    };
+    if (anchors) add(sA, 16, 0, true);
+    // backwards: chunks nch - 1 and nch - 2 are still there
+#pragma unroll 1
+    for (int ch = nch - 1; ch >= 0; --ch) {
+      if (ch < nch - 1) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // chunk ch is there, chunk ch + 1 has been read
+        if (ch > 0) stage(ch - 1);
+      }
+      const int cs = cs0 + ch * CK;
+#pragma unroll 1
+      for (int kb = first_block(cs); wlive && kb <= min(cs + CK - 1, kmax);
+           kb += 32)
+        add(sC + (ch & 1) * SM::chunk + (kb - cs) * RS, CK, kb, false);
     }
-    __syncwarp();
-    bf* dQ = reinterpret_cast<bf*>(a.dQ) + (rowbase + i0) * D;
-    for (int e = lane; e < 16 * (D / 8); e += 32)
-      if (e / (D / 8) < nrow)
-        reinterpret_cast<uint4*>(dQ)[e] = pack16<bf>(s_dq + e * 8);
   }
+  // dQ: the listed part, then the two warps' window parts, in this order
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    if (u == hf) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float2* pa = reinterpret_cast<float2*>(
+            s_dq + (rg * 16 + gr) * DS + 8 * t + 2 * tq);
+        float2* pb = pa + 4 * DS;
+        const float2 x = *pa, y = *pb;
+        *pa = make_float2(x.x + o[t][0], x.y + o[t][1]);
+        *pb = make_float2(y.x + o[t][2], y.y + o[t][3]);
+      }
+    }
+    __syncthreads();
+  }
+  bf* dQ = reinterpret_cast<bf*>(a.dQ) + (rowbase + r0) * D;
+  const int live = min(64, nq - r0);
+  for (int e = threadIdx.x; e < live * (D / 8); e += kRowWarps * 32)
+    reinterpret_cast<uint4*>(dQ)[e] =
+        pack16<bf>(s_dq + e / (D / 8) * DS + e % (D / 8) * 8);
 }
 
 // ------------------------------------------------------------- column pass
@@ -723,11 +805,7 @@ backward_columns_mma(Args a, int ntile) {
         const int rl = rb + (lane & 15);
         if (!__any_sync(kAll, a.p0 + rc + rl >= kw && s_lo[rl] <= kw + 15))
           continue;
-        float x[2][4], dp[2][4];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[t][c] = dp[t][c] = 0.f;
+        float x[2][4] = {}, dp[2][4] = {};
         const int ar = wid * 16 + (lane & 15), ac = (lane >> 4) * 16;
         const int br = rb + (lane & 7) + ((lane >> 4) << 3);
         const int bc = ((lane >> 3) & 1) * 16;
@@ -753,7 +831,7 @@ backward_columns_mma(Args a, int ntile) {
             const int rl2 = rb + 8 * t + 2 * tq + (c & 1);
             const int j = kw + gr + (c >= 2 ? 8 : 0);
             const bool ok = j <= a.p0 + rc + rl2 && j >= s_lo[rl2];
-            const float p = ok ? exp2f(x[t][c] * sl2 - s_lse[rl2]) : 0.f;
+            const float p = ok ? ex2(x[t][c] * sl2 - s_lse[rl2]) : 0.f;
             x[t][c] = p;
             dp[t][c] = p * (dp[t][c] - s_D[rl2]) * sc;
           }
