@@ -61,8 +61,6 @@ class CaNormRope(ctypes.Structure):
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _X = ctypes.POINTER(CaExtras)
-_R = ctypes.POINTER(CaRows)
-_N = ctypes.POINTER(CaNormRope)
 SIGNATURES = {
     "condensate_attn_workspace_size":
         (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
@@ -96,10 +94,10 @@ SIGNATURES = {
     "condensate_attn_decode_shard_combine":
         (_I, [_P, _I, _I, _I, _I, _P, _I, _P]),
     "condensate_attn_norm_rope":
-        (_I, [_R, _I, _I, _I, _I, _I, _I, _N, _R, _P]),
+        (_I, [_P, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
     "condensate_attn_norm_rope_workspace_size": (ctypes.c_size_t, [_I]),
     "condensate_attn_norm_rope_backward":
-        (_I, [_R, _R, _I, _I, _I, _I, _I, _I, _N, _R, _P, _P, _P,
+        (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
               ctypes.c_size_t, _P]),
     "condensate_attn_prefill_backward_workspace_size":
         (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),

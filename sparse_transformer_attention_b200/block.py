@@ -15,38 +15,50 @@ captured into CUDA graphs.
 """
 from __future__ import annotations
 
-import contextlib
-import ctypes
+import struct
 from typing import Optional, Tuple
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding
-from .binding import CaNormRope, CaRows, _check, _dt, _ptr, _require
+from .binding import _check, _dt, _ptr, _require
 
 _DTYPES = (torch.float32, torch.bfloat16)
 
 
-@contextlib.contextmanager
-def _on(dev: torch.device, stream):
-    """The raw stream to launch on, with `dev` current and what is allocated
-    inside belonging to that stream."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, tensors on {dev}")
-        with torch.cuda.stream(stream):
-            yield ctypes.c_void_p(stream.cuda_stream)
-    elif torch.cuda.current_device() == dev.index:
-        yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+class _On:
+    """`dev` current, and what is allocated inside belonging to `stream`; as
+    a value, the raw stream to launch on."""
+    __slots__ = ("raw", "guard")
+
+    def __init__(self, dev: torch.device, stream):
+        self.guard = None
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(
+                    f"stream is on {stream.device}, tensors on {dev}")
+            self.guard = torch.cuda.stream(stream)
+            self.raw = stream.cuda_stream
+        else:
+            if torch.cuda.current_device() != dev.index:
+                self.guard = torch.cuda.device(dev)
+            # torch.cuda.current_stream(dev).cuda_stream without the object
+            self.raw = torch._C._cuda_getCurrentRawStream(dev.index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.raw
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def _expect(t: torch.Tensor, name: str, shape, dtype, dev):
     """Shape, type and device of one argument."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, "
                          f"got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
@@ -60,22 +72,40 @@ def _dense(t: torch.Tensor, name: str, shape, dtype, dev):
     _require(t, name)
 
 
-def _grid(t: Optional[torch.Tensor], head_major: bool, name: str):
-    """ca_rows of a [B, n, H, d] tensor ([B, H, n, d] when head_major)."""
+# ca_rows[3] and ca_norm_rope of the header as packed bytes (a third of the
+# time that ctypes takes to fill the structures, which counts in a decode)
+_ROWS3 = struct.Struct("12q")
+_PARAMS = struct.Struct("PPifPiiPi4x")
+_NONE = (0, 0, 0, 0)
+
+
+def _token_major(t: Optional[torch.Tensor], name: str):
+    """The ca_rows fields of a [B, n, H, d] tensor."""
     if t is None:
-        return CaRows()
-    sb, s1, s2, sd = t.stride()
-    B, n1, n2, _ = t.shape
+        return _NONE
+    sb, st, sh, sd = t.stride()
+    B, n, H, _ = t.shape
     if sd != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     # the stride of a dimension of one element says nothing
-    sb, s1, s2 = sb if B > 1 else 0, s1 if n1 > 1 else 0, s2 if n2 > 1 else 0
-    return CaRows(t.data_ptr(), sb, s2, s1) if head_major else \
-        CaRows(t.data_ptr(), sb, s1, s2)
+    return (t.data_ptr(), sb if B > 1 else 0, st if n > 1 else 0,
+            sh if H > 1 else 0)
+
+
+def _head_major(t: Optional[torch.Tensor], name: str):
+    """The ca_rows fields of a [B, H, n, d] tensor."""
+    if t is None:
+        return _NONE
+    sb, sh, st, sd = t.stride()
+    B, H, n, _ = t.shape
+    if sd != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return (t.data_ptr(), sb if B > 1 else 0, st if n > 1 else 0,
+            sh if H > 1 else 0)
 
 
 def _rope_params(d, n_tokens, dev, inv_freq, q_weight, k_weight, eps,
-                 positions, pos0, interleaved) -> CaNormRope:
+                 positions, pos0, interleaved) -> bytes:
     w_dtype = None
     for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
@@ -90,13 +120,15 @@ def _rope_params(d, n_tokens, dev, inv_freq, q_weight, k_weight, eps,
         _dense(inv_freq, "inv_freq", (rot // 2,), torch.float32, dev)
     if positions is not None:
         _dense(positions, "positions", n_tokens, torch.int32, dev)
-    return CaNormRope(
-        None if q_weight is None else q_weight.data_ptr(),
-        None if k_weight is None else k_weight.data_ptr(),
-        binding.CA_F32 if w_dtype is None else _dt(w_dtype), eps,
-        None if inv_freq is None else inv_freq.data_ptr(), rot,
-        int(interleaved),
-        None if positions is None else positions.data_ptr(), pos0)
+    if not -(1 << 31) <= pos0 < 1 << 31:
+        raise ValueError("pos0 must fit 32 bits")
+    return _PARAMS.pack(
+        0 if q_weight is None else q_weight.data_ptr(),
+        0 if k_weight is None else k_weight.data_ptr(),
+        binding.CA_BF16 if w_dtype is torch.bfloat16 else binding.CA_F32,
+        eps, 0 if inv_freq is None else inv_freq.data_ptr(), rot,
+        1 if interleaved else 0,
+        0 if positions is None else positions.data_ptr(), pos0)
 
 
 def _sizes(q, k, v):
@@ -140,7 +172,7 @@ def condensate_attn_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor],
     dev = q.device
     par = _rope_params(d, (B, n), dev, inv_freq, q_weight, k_weight, eps,
                        positions, pos0, interleaved)
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         outs = []
         for x, y, H, nm in ((q, Q, Hq, "Q"), (k, K, Hkv, "K"),
                             (v, V, Hkv, "V")):
@@ -153,11 +185,12 @@ def condensate_attn_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor],
                 _expect(y, nm, (B, H, n, d), q.dtype, dev)
             outs.append(y)
         code = binding.load().condensate_attn_norm_rope(
-            (CaRows * 3)(_grid(q, False, "q"), _grid(k, False, "k"),
-                         _grid(v, False, "v")),
-            _dt(q.dtype), B, n, Hq, Hkv, d, ctypes.byref(par),
-            (CaRows * 3)(_grid(outs[0], True, "Q"), _grid(outs[1], True, "K"),
-                         _grid(outs[2], True, "V")), s)
+            _ROWS3.pack(*_token_major(q, "q"), *_token_major(k, "k"),
+                        *_token_major(v, "v")),
+            _dt(q.dtype), B, n, Hq, Hkv, d, par,
+            _ROWS3.pack(*_head_major(outs[0], "Q"),
+                        *_head_major(outs[1], "K"),
+                        *_head_major(outs[2], "V")), s)
     _check(code, "condensate_attn_norm_rope")
     return tuple(outs)
 
@@ -200,7 +233,7 @@ def condensate_attn_norm_rope_backward(
         k if k_weight is not None else None
     par = _rope_params(d, (B, n), dev, inv_freq, q_weight, k_weight, eps,
                        positions, pos0, interleaved)
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         outs = []
         for g, x, H, nm in ((dQ, dq, Hq, "dq"), (dK, dk, Hkv, "dk"),
                             (dV, dv, Hkv, "dv")):
@@ -224,13 +257,14 @@ def condensate_attn_norm_rope_backward(
         if workspace is not None:
             _require(workspace, "workspace")
         code = lib.condensate_attn_norm_rope_backward(
-            (CaRows * 3)(_grid(dQ, True, "dQ"), _grid(dK, True, "dK"),
-                         _grid(dV, True, "dV")),
-            (CaRows * 3)(_grid(q, False, "q"), _grid(k, False, "k")),
-            _dt(dt), B, n, Hq, Hkv, d, ctypes.byref(par),
-            (CaRows * 3)(_grid(outs[0], False, "dq"),
-                         _grid(outs[1], False, "dk"),
-                         _grid(outs[2], False, "dv")),
+            _ROWS3.pack(*_head_major(dQ, "dQ"), *_head_major(dK, "dK"),
+                        *_head_major(dV, "dV")),
+            _ROWS3.pack(*_token_major(q, "q"), *_token_major(k, "k"),
+                        *_NONE),
+            _dt(dt), B, n, Hq, Hkv, d, par,
+            _ROWS3.pack(*_token_major(outs[0], "dq"),
+                        *_token_major(outs[1], "dk"),
+                        *_token_major(outs[2], "dv")),
             _ptr(dqw), _ptr(dkw), _ptr(workspace),
             0 if workspace is None else workspace.numel() *
             workspace.element_size(), s)
@@ -278,7 +312,7 @@ def condensate_attn_prefill_backward(
         _dense(W_i, "W_i", (B, nq), torch.int32, dev)
     if W_h is not None:
         _dense(W_h, "W_h", (Hq,), torch.int32, dev)
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         if dQ is None:
             dQ = torch.empty_like(Q)
         if dK is None:

@@ -67,30 +67,25 @@ bool plan(Work& w, bool planes, int B, int nq, int L, int Hq, int Hkv, int d,
   return true;
 }
 
-// Per batch row, the largest window; per chunk of rows, the lowest window
-// start: what lets the column pass skip rows that cannot reach its keys.
-__global__ void backward_windows(Args a) {
-  const int b = blockIdx.y, chunks = gridDim.x;
-  __shared__ int s_w[2], s_lo[2];
-  const int r = blockIdx.x * kRowChunk + threadIdx.x;  // kRowChunk threads
+// Per batch row, the largest window; per chunk of rows (a warp each), the
+// lowest window start: what lets the column pass skip rows that cannot reach
+// its keys.
+__global__ void backward_windows(Args a, int chunks) {
+  static_assert(kRowChunk == 32, "a lane per row");
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int chunk = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+  if (chunk >= chunks) return;
+  const int r = chunk * kRowChunk + lane;
   int w = 1, lo = 0x7FFFFFFF;
   if (r < a.nq) {
     w = min(max(a.W_i[(int64_t)b * a.nq + r], 1), a.L);
     lo = max(a.p0 + r - w + 1, 0);
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    w = max(w, __shfl_xor_sync(kAll, w, off));
-    lo = min(lo, __shfl_xor_sync(kAll, lo, off));
-  }
-  if ((threadIdx.x & 31) == 0) {
-    s_w[threadIdx.x >> 5] = w;
-    s_lo[threadIdx.x >> 5] = lo;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    atomicMax(a.wmax + b, max(s_w[0], s_w[1]));
-    a.lows[b * chunks + blockIdx.x] = min(s_lo[0], s_lo[1]);
+  w = __reduce_max_sync(kAll, w);
+  lo = __reduce_min_sync(kAll, lo);
+  if (lane == 0) {
+    atomicMax(a.wmax + b, w);
+    a.lows[(int64_t)b * chunks + chunk] = lo;
   }
 }
 
@@ -481,9 +476,11 @@ cudaError_t launch_as(Args a, cudaStream_t s) {
   constexpr bool kMma = sizeof(T) == 2;  // bf16: the tensor-core kernels
   const Work& w = a.w;
   cudaError_t e = cudaSuccess;
-  if (a.W_i)
-    e = run("backward_windows", backward_windows,
-            dim3((a.nq + kRowChunk - 1) / kRowChunk, a.B), kRowChunk, 0, s, a);
+  if (a.W_i) {
+    const int chunks = (a.nq + kRowChunk - 1) / kRowChunk;
+    e = run("backward_windows", backward_windows, dim3((chunks + 7) / 8, a.B),
+            256, 0, s, a, chunks);
+  }
   if (e != cudaSuccess) return e;
   if constexpr (kMma) {
     if (a.do_bf16) {

@@ -16,7 +16,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // in the order of idx; unused slots hold key L, which sorts behind all keys.
 constexpr int kTile = 4096;   // entries per CTA of the sort
 constexpr int kRange = 64;    // sorted entries of a sum of the listed pass
-constexpr int kRowChunk = 64; // query rows staged at a time by the columns
+constexpr int kRowChunk = 32; // query rows staged at a time by the columns
 
 struct Work {
   int64_t rows;      // B * Hq * nq

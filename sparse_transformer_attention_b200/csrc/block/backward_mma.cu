@@ -70,9 +70,6 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
                "l"(src)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
-}
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -717,32 +714,46 @@ backward_rows_mma(Args a, int ntile) {
 // ------------------------------------------------------------- column pass
 // A CTA owns 64 keys of one kv head, a warp 16: S^T and dP^T of 16 keys x 16
 // rows at a time, then dV += P^T dO and dK += dS^T Q with P^T and dS^T in two
-// parts straight from their accumulators.  Query rows are staged 64 at a
-// time with their log-sum-exp, D and window start; the listed part is added
-// at the end.
+// parts straight from their accumulators.  Query rows are staged kRowChunk
+// at a time with their log-sum-exp, D and window, the next chunk (of the
+// group's next head at a head's end) while the current one is used; the
+// listed part is added at the end.
 constexpr int kColWarps = 4;
 
 template <int D, int NP>
 struct ColSmem {
+  static constexpr int RC = kRowChunk;
   static constexpr int RS = D * 2 + 16;
-  static constexpr size_t tile = (size_t)64 * RS;
-  static constexpr size_t bytes = (3 + NP) * tile + 64 * 12;
+  static constexpr size_t keys = (size_t)64 * RS;
+  static constexpr size_t rows = (size_t)RC * RS;
+  // K, V; two buffers of q, the planes of dO, (log-sum-exp, D) and windows
+  static constexpr size_t buffer = (1 + NP) * rows + RC * 12;
+  static constexpr size_t bytes = 2 * keys + 2 * buffer;
 };
+
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
 
 template <int D, int NP>
 __global__ void __launch_bounds__(kColWarps * 32)
 backward_columns_mma(Args a, int ntile) {
   using SM = ColSmem<D, NP>;
-  constexpr int RS = SM::RS;
+  constexpr int RS = SM::RS, RC = SM::RC;
   constexpr int KS = D / 16, NT = D / 8;
   extern __shared__ __align__(16) unsigned char g_smem[];
   unsigned char* sK = g_smem;
-  unsigned char* sV = sK + SM::tile;
-  unsigned char* sQ = sV + SM::tile;
-  unsigned char* sG = sQ + SM::tile;  // NP planes
-  float* s_lse = reinterpret_cast<float*>(sG + NP * SM::tile);
-  float* s_D = s_lse + 64;
-  int* s_lo = reinterpret_cast<int*>(s_D + 64);
+  unsigned char* sV = sK + SM::keys;
+  unsigned char* sB = sV + SM::keys;  // two buffers
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int gr = lane >> 2, tq = lane & 3;
   const int L = a.L, nq = a.nq, G = a.Hq / a.Hkv;
@@ -752,119 +763,155 @@ backward_columns_mma(Args a, int ntile) {
   const int kw = j0 + wid * 16;  // the warp's first key
   const float sl2 = kLog2e / sqrtf((float)D), sc = 1.f / sqrtf((float)D);
   constexpr int kPieces = D * 2 / 16;
-  auto stage = [&](unsigned char* dst, const bf* src, int first, int limit) {
-    for (int e = threadIdx.x; e < 64 * kPieces; e += kColWarps * 32) {
+  auto copy_rows = [&](unsigned char* dst, const bf* src, int first, int count,
+                       int limit) {
+    for (int e = threadIdx.x; e < count * kPieces; e += kColWarps * 32) {
       const int rr = e / kPieces, pc = e % kPieces;
       cp_async16(dst + rr * RS + pc * 16,
                  src + (int64_t)min(first + rr, limit - 1) * D + pc * 8);
     }
   };
-  stage(sK, reinterpret_cast<const bf*>(a.K) + (int64_t)seg * L * D, j0, L);
-  stage(sV, reinterpret_cast<const bf*>(a.V) + (int64_t)seg * L * D, j0, L);
+  // The chunks of rows that see any of the CTA's keys: (head, first row).
+  const int jl = min(j0 + 63, L - 1);  // the CTA's last key
+  const int chunks = (nq + RC - 1) / RC;
+  int hh = -1, rc = 0, rmax = -1;  // head of the group, chunk, its last row
+  auto advance = [&]() {
+    rc += RC;
+    while (true) {
+      for (; rc <= rmax; rc += RC)
+        if (!a.W_i || a.lows[(int64_t)b * chunks + rc / RC] <= jl) return true;
+      if (++hh >= G) return false;
+      int wm = a.W_i ? a.wmax[b] : (a.W_h ? a.W_h[g * G + hh] : a.W);
+      wm = min(max(wm, 1), L);
+      // rows whose position i has i - wm + 1 <= jl and i >= j0
+      rc = max(j0 - a.p0, 0) / RC * RC;
+      rmax = (int)min((int64_t)jl + wm - 1 - a.p0, (int64_t)nq - 1);
+    }
+  };
+  auto stage = [&](int buf) {
+    unsigned char* dst = sB + buf * SM::buffer;
+    const int h = g * G + hh;
+    const int64_t rowbase = ((int64_t)b * a.Hq + h) * nq;
+    copy_rows(dst, reinterpret_cast<const bf*>(a.Q) + rowbase * D, rc, RC, nq);
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+      copy_rows(dst + (p + 1) * SM::rows, a.g[p] + rowbase * D, rc, RC, nq);
+    if (threadIdx.x < RC) {
+      float2* st = reinterpret_cast<float2*>(dst + (1 + NP) * SM::rows);
+      int* sw = reinterpret_cast<int*>(st + RC);
+      const int r = min(rc + (int)threadIdx.x, nq - 1);
+      cp_async8(st + threadIdx.x, a.stats + rowbase + r);
+      if (a.W_i)
+        cp_async4(sw + threadIdx.x, a.W_i + (int64_t)b * nq + r);
+      else
+        sw[threadIdx.x] = a.W_h ? a.W_h[h] : a.W;
+    }
+  };
+  copy_rows(sK, reinterpret_cast<const bf*>(a.K) + (int64_t)seg * L * D, j0, 64,
+            L);
+  copy_rows(sV, reinterpret_cast<const bf*>(a.V) + (int64_t)seg * L * D, j0, 64,
+            L);
   float dk[NT][4], dv[NT][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int c = 0; c < 4; ++c) dk[t][c] = dv[t][c] = 0.f;
-  const int jl = min(j0 + 63, L - 1);  // the CTA's last key
-  const int chunks = (nq + kRowChunk - 1) / kRowChunk;
+  const int imax = a.p0 + nq - 1;
+  bool more = advance();
+  if (more) stage(0);
+  asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll 1
-  for (int hh = 0; hh < G; ++hh) {
-    const int h = g * G + hh;
-    int wm = a.W_i ? a.wmax[b] : (a.W_h ? a.W_h[h] : a.W);
-    wm = min(max(wm, 1), L);
-    // rows whose position i has i - wm + 1 <= jl and i >= j0
-    const int rmin = max(j0 - a.p0, 0);
-    const int rmax = (int)min((int64_t)jl + wm - 1 - a.p0, (int64_t)nq - 1);
-    const int64_t rowbase = ((int64_t)b * a.Hq + h) * nq;
+  for (int buf = 0; more; buf ^= 1) {
+    const int i0 = a.p0 + rc;  // position of the chunk's first row
+    more = advance();
+    if (more) stage(buf ^ 1);
+    asm volatile("cp.async.commit_group;\ncp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    const unsigned char* sQ = sB + buf * SM::buffer;
+    const unsigned char* sG = sQ + SM::rows;
+    const float2* s_st =
+        reinterpret_cast<const float2*>(sQ + (1 + NP) * SM::rows);
+    const int* s_w = reinterpret_cast<const int*>(s_st + RC);
 #pragma unroll 1
-    for (int rc = rmin / 64 * 64; rc <= rmax; rc += 64) {
-      if (a.W_i && a.lows[b * chunks + rc / 64] > jl) continue;
-      __syncthreads();  // the last chunk has been read
-      stage(sQ, reinterpret_cast<const bf*>(a.Q) + rowbase * D, rc, nq);
-#pragma unroll
-      for (int p = 0; p < NP; ++p)
-        stage(sG + p * SM::tile, a.g[p] + rowbase * D, rc, nq);
-      if (threadIdx.x < 64) {
-        const int r = rc + threadIdx.x;
-        int w, lo = 0x7FFFFFFF;  // rows behind the last: no key
-        float2 st = make_float2(0.f, 0.f);
-        if (r < nq) {
-          lo = window_lo(a, b, h, r, false, &w);
-          st = a.stats[rowbase + r];
-        }
-        s_lo[threadIdx.x] = lo;
-        s_lse[threadIdx.x] = st.x;
-        s_D[threadIdx.x] = st.y;
-      }
-      cp_async_wait_all();
-      __syncthreads();
-#pragma unroll 1
-      for (int rb = 0; rb < 64; rb += 16) {
-        // does any of these 16 rows see any of the warp's 16 keys?
-        const int rl = rb + (lane & 15);
-        if (!__any_sync(kAll, a.p0 + rc + rl >= kw && s_lo[rl] <= kw + 15))
-          continue;
-        float x[2][4] = {}, dp[2][4] = {};
-        const int ar = wid * 16 + (lane & 15), ac = (lane >> 4) * 16;
-        const int br = rb + (lane & 7) + ((lane >> 4) << 3);
-        const int bc = ((lane >> 3) & 1) * 16;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          uint32_t A[4], B[4];
-          ldsm4(A, sK + ar * RS + ks * 32 + ac);
-          ldsm4(B, sQ + br * RS + ks * 32 + bc);
-          mma(x[0], A[0], A[1], A[2], A[3], B[0], B[1]);
-          mma(x[1], A[0], A[1], A[2], A[3], B[2], B[3]);
-          ldsm4(A, sV + ar * RS + ks * 32 + ac);
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            ldsm4(B, sG + p * SM::tile + br * RS + ks * 32 + bc);
-            mma(dp[0], A[0], A[1], A[2], A[3], B[0], B[1]);
-            mma(dp[1], A[0], A[1], A[2], A[3], B[2], B[3]);
-          }
-        }
+    for (int rb = 0; rb < RC; rb += 16) {
+      // do these 16 rows see any, or all, of the warp's 16 keys?
+      const int il = i0 + rb + (lane & 15);
+      const int wl = max(s_w[rb + (lane & 15)], 1);
+      if (!__any_sync(kAll, il >= kw && il <= imax && il - (kw + 15) < wl))
+        continue;
+      const bool inner =
+          __all_sync(kAll, il >= kw + 15 && il <= imax && il - kw < wl);
+      float x[2][4], dp[2][4];
+      const int ar = wid * 16 + (lane & 15), ac = (lane >> 4) * 16;
+      const int br = rb + (lane & 7) + ((lane >> 4) << 3);
+      const int bc = ((lane >> 3) & 1) * 16;
+      auto step = [&](float (&d)[2][4], const uint32_t (&A)[4],
+                      const unsigned char* bp, bool first) {
+        uint32_t f[4];
+        ldsm4(f, bp);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
+          if (first) mma0(d[t], A[0], A[1], A[2], A[3], f[2 * t], f[2 * t + 1]);
+          else mma(d[t], A[0], A[1], A[2], A[3], f[2 * t], f[2 * t + 1]);
+      };
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int rl2 = rb + 8 * t + 2 * tq + (c & 1);
-            const int j = kw + gr + (c >= 2 ? 8 : 0);
-            const bool ok = j <= a.p0 + rc + rl2 && j >= s_lo[rl2];
-            const float p = ok ? ex2(x[t][c] * sl2 - s_lse[rl2]) : 0.f;
-            x[t][c] = p;
-            dp[t][c] = p * (dp[t][c] - s_D[rl2]) * sc;
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t A[4];
+        ldsm4(A, sK + ar * RS + ks * 32 + ac);
+        step(x, A, sQ + br * RS + ks * 32 + bc, ks == 0);
+        ldsm4(A, sV + ar * RS + ks * 32 + ac);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+          step(dp, A, sG + p * SM::rows + br * RS + ks * 32 + bc,
+               ks == 0 && p == 0);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int rl = rb + 8 * t + 2 * tq + c;
+          const float2 st = s_st[rl];
+          const int i = i0 + rl, w = max(s_w[rl], 1);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int j = kw + gr + 8 * u;
+            const bool ok = inner || (j <= i && i <= imax && i - j < w);
+            const float p =
+                ok ? ex2(fmaf(x[t][c + 2 * u], sl2, -st.x)) : 0.f;
+            x[t][c + 2 * u] = p;
+            dp[t][c + 2 * u] = p * (dp[t][c + 2 * u] - st.y) * sc;
           }
-        uint32_t ph[4], pl[4], dh[4], dl[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          split2(x[c >> 1][(c & 1) * 2], x[c >> 1][(c & 1) * 2 + 1], &ph[c],
-                 &pl[c]);
-          split2(dp[c >> 1][(c & 1) * 2], dp[c >> 1][(c & 1) * 2 + 1], &dh[c],
-                 &dl[c]);
         }
-        const int tr = (rb + (lane & 15)) * RS + (lane >> 4) * 16;
+      uint32_t ph[4], pl[4], dh[4], dl[4];
 #pragma unroll
-        for (int t = 0; t < NT; t += 2) {
-          uint32_t f[4];
-          ldsm4t(f, sQ + tr + t * 16);
-          mma(dk[t], dh[0], dh[1], dh[2], dh[3], f[0], f[1]);
-          mma(dk[t], dl[0], dl[1], dl[2], dl[3], f[0], f[1]);
-          mma(dk[t + 1], dh[0], dh[1], dh[2], dh[3], f[2], f[3]);
-          mma(dk[t + 1], dl[0], dl[1], dl[2], dl[3], f[2], f[3]);
+      for (int c = 0; c < 4; ++c) {
+        split2(x[c >> 1][(c & 1) * 2], x[c >> 1][(c & 1) * 2 + 1], &ph[c],
+               &pl[c]);
+        split2(dp[c >> 1][(c & 1) * 2], dp[c >> 1][(c & 1) * 2 + 1], &dh[c],
+               &dl[c]);
+      }
+      const int tr = (rb + (lane & 15)) * RS + (lane >> 4) * 16;
 #pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            ldsm4t(f, sG + p * SM::tile + tr + t * 16);
-            mma(dv[t], ph[0], ph[1], ph[2], ph[3], f[0], f[1]);
-            mma(dv[t + 1], ph[0], ph[1], ph[2], ph[3], f[2], f[3]);
-            if (p == 0) {  // lo x lo is below what two parts keep
-              mma(dv[t], pl[0], pl[1], pl[2], pl[3], f[0], f[1]);
-              mma(dv[t + 1], pl[0], pl[1], pl[2], pl[3], f[2], f[3]);
-            }
+      for (int t = 0; t < NT; t += 2) {
+        uint32_t f[4];
+        ldsm4t(f, sQ + tr + t * 16);
+        mma(dk[t], dh[0], dh[1], dh[2], dh[3], f[0], f[1]);
+        mma(dk[t + 1], dh[0], dh[1], dh[2], dh[3], f[2], f[3]);
+        mma(dk[t], dl[0], dl[1], dl[2], dl[3], f[0], f[1]);
+        mma(dk[t + 1], dl[0], dl[1], dl[2], dl[3], f[2], f[3]);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          ldsm4t(f, sG + p * SM::rows + tr + t * 16);
+          mma(dv[t], ph[0], ph[1], ph[2], ph[3], f[0], f[1]);
+          mma(dv[t + 1], ph[0], ph[1], ph[2], ph[3], f[2], f[3]);
+          if (p == 0) {  // lo x lo is below what two parts keep
+            mma(dv[t], pl[0], pl[1], pl[2], pl[3], f[0], f[1]);
+            mma(dv[t + 1], pl[0], pl[1], pl[2], pl[3], f[2], f[3]);
           }
         }
       }
     }
+    __syncthreads();  // the buffer may be written again
   }
   asm volatile("cp.async.wait_all;" ::: "memory");  // K and V, if unused
   __syncthreads();
@@ -874,8 +921,8 @@ backward_columns_mma(Args a, int ntile) {
   // the whole CTA, in a fixed order.
   constexpr int kShort = 4;
   constexpr int kCols = 2 * D / 4, kParts = kColWarps * 32 / kCols;
-  int2* s_span = reinterpret_cast<int2*>(sQ);
-  float4* s_sum = reinterpret_cast<float4*>(sQ + 64 * 8);  // [parts][2 D]
+  int2* s_span = reinterpret_cast<int2*>(sB);
+  float4* s_sum = reinterpret_cast<float4*>(sB + 64 * 8);  // [parts][2 D]
   if (threadIdx.x < 64)
     s_span[threadIdx.x] = j0 + threadIdx.x < L
                               ? a.span[(int64_t)seg * L + j0 + threadIdx.x]

@@ -154,3 +154,17 @@ def test_binding_refuses_cpu_tensors(lib):
         ca.condensate_attn_prefill_backward(y, y, y, y, i, i[..., 0], 4, 2)
     with pytest.raises(ValueError):
         ca.qkv_attention(torch.zeros(1, 4, 100), 2, 1, 4, 2, None)
+
+
+def test_packed_structures():
+    """The binding's packed bytes have the header's layout."""
+    from sparse_transformer_attention_b200 import block
+    rows = (CaRows * 3)(*(CaRows(16 * i + 16, 3 * i, 3 * i + 1, 3 * i + 2)
+                          for i in range(3)))
+    packed = block._ROWS3.pack(*(x for r in rows for x in (
+        r.data, r.stride_b, r.stride_t, r.stride_h)))
+    assert packed == bytes(rows)
+    p = CaNormRope(16, 32, 1, 0.5, 48, 64, 1, 80, -7)
+    packed = block._PARAMS.pack(16, 32, 1, 0.5, 48, 64, 1, 80, -7)
+    assert len(packed) == ctypes.sizeof(p)
+    assert bytes(CaNormRope.from_buffer_copy(packed)) == bytes(p)
