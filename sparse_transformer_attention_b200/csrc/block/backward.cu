@@ -16,8 +16,6 @@
 // so a key's rows stay in ascending order), a pass over the sorted slots
 // sums each key's listed part, and the column pass adds its window part.  No
 // sum depends on timing: every order of addition is fixed by the inputs.
-#include "../launch.cuh"
-#include "../profile.cuh"
 #include "backward.cuh"
 
 namespace ca {
@@ -50,6 +48,7 @@ bool plan(Work& w, bool planes, int B, int nq, int L, int Hq, int Hkv, int d,
     return a;
   };
   w.wmax = take((size_t)B * 4);
+  w.span = take((size_t)w.segs * L * 8);
   w.lows = take((size_t)B * ((nq + kRowChunk - 1) / kRowChunk) * 4);
   w.stats = take((size_t)w.rows * 8);
   w.pds = take(n * 8);
@@ -59,7 +58,6 @@ bool plan(Work& w, bool planes, int B, int nq, int L, int Hq, int Hkv, int d,
   }
   w.hist = take((size_t)w.segs * 256 * w.tiles * 4);
   w.totals = take((size_t)w.segs * 256 * 4);
-  w.span = take((size_t)w.segs * L * 8);
   w.top = take((size_t)w.segs * L * 2 * d * 4);
   w.carry = take((size_t)w.segs * w.ranges * 2 * d * 4);
   w.planes = take(planes ? (size_t)w.rows * d * 4 : 0);
@@ -71,6 +69,7 @@ bool plan(Work& w, bool planes, int B, int nq, int L, int Hq, int Hkv, int d,
 // lowest window start: what lets the column pass skip rows that cannot reach
 // its keys.
 __global__ void backward_windows(Args a, int chunks) {
+  chain();
   static_assert(kRowChunk == 32, "a lane per row");
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int chunk = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
@@ -92,6 +91,7 @@ __global__ void backward_windows(Args a, int chunks) {
 // An fp32 dO as two bf16 planes (see Args::g).
 __global__ void __launch_bounds__(256)
 backward_split(const float4* x, uint2* hi, uint2* lo, int64_t n4) {
+  chain();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n4) return;
   const float4 v = x[i];
@@ -150,6 +150,7 @@ template <typename T, typename TD, int D>
 __global__ void __launch_bounds__(kRowWarps * 32) backward_rows(Args a) {
   constexpr int DL = D / 8;
   extern __shared__ __align__(16) unsigned char g_smem[];
+  chain();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int sub = lane & 7, grp = lane >> 3;
   float2* s_x = reinterpret_cast<float2*>(g_smem) + wid * (a.k + 1);
@@ -274,6 +275,7 @@ backward_listed(Args a, const uint32_t* keys, const uint32_t* ents) {
   constexpr int SUBS = 32 / LPR;         // ranges per warp
   constexpr int U = 4;                   // entries read at a time
   __shared__ uint4 s_ent[kListedWarps][SUBS * kRange];
+  chain();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int sub = lane / LPR, sl = lane % LPR;
   const int seg = blockIdx.y;
@@ -383,6 +385,7 @@ backward_listed(Args a, const uint32_t* keys, const uint32_t* ents) {
 template <typename T, typename TD, int D>
 __global__ void __launch_bounds__(256) backward_columns(Args a) {
   constexpr int DL = D / 8;
+  chain();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int sub = lane & 7, grp = lane >> 3;
   const int64_t col = (int64_t)blockIdx.x * 8 + wid;
@@ -462,15 +465,6 @@ __global__ void __launch_bounds__(256) backward_columns(Args a) {
 }
 
 // --------------------------------------------------------------- host side
-template <typename F, typename... P>
-cudaError_t run(const char* name, F* kern, dim3 grid, int threads, size_t smem,
-                cudaStream_t s, P... p) {
-  prof_before(s, name);
-  kern<<<grid, threads, smem, s>>>(p...);
-  prof_after(s);
-  return cudaGetLastError();
-}
-
 template <typename T, typename TD, int D>
 cudaError_t launch_as(Args a, cudaStream_t s) {
   constexpr bool kMma = sizeof(T) == 2;  // bf16: the tensor-core kernels
@@ -478,7 +472,7 @@ cudaError_t launch_as(Args a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (a.W_i) {
     const int chunks = (a.nq + kRowChunk - 1) / kRowChunk;
-    e = run("backward_windows", backward_windows, dim3((chunks + 7) / 8, a.B),
+    e = launch("backward_windows", backward_windows, dim3((chunks + 7) / 8, a.B),
             256, 0, s, a, chunks);
   }
   if (e != cudaSuccess) return e;
@@ -488,32 +482,30 @@ cudaError_t launch_as(Args a, cudaStream_t s) {
       a.g[1] = nullptr;
     } else {
       const int64_t n4 = w.rows * D / 4;
-      e = run("backward_split", backward_split,
+      e = launch("backward_split", backward_split,
               dim3((unsigned)((n4 + 255) / 256)), 256, 0, s,
               (const float4*)a.dO, (uint2*)a.g[0], (uint2*)a.g[1], n4);
       if (e != cudaSuccess) return e;
     }
     e = rows_mma_launch(a, D, s);
   } else {
-    e = run("backward_rows", backward_rows<T, TD, D>,
+    e = launch("backward_rows", backward_rows<T, TD, D>,
             dim3((unsigned)((w.rows + kRowWarps - 1) / kRowWarps)),
             kRowWarps * 32, (size_t)kRowWarps * (a.k + 1) * 8, s, a);
   }
   if (e != cudaSuccess) return e;
   int last;
   if ((e = sort_launch(a, &last, s)) != cudaSuccess) return e;
-  e = cudaMemsetAsync(a.span, 0, (size_t)w.segs * a.L * 8, s);
-  if (e != cudaSuccess) return e;
   const uint32_t *keys = a.key[last], *ents = a.ent[last];
   constexpr int kPer = kListedWarps * 32 * Elem<T>::kPer16B / D;  // ranges
-  e = run("backward_listed", backward_listed<T, TD, D>,
+  e = launch("backward_listed", backward_listed<T, TD, D>,
           dim3((w.ranges + kPer - 1) / kPer, w.segs), kListedWarps * 32, 0, s,
           a, keys, ents);
   if (e != cudaSuccess) return e;
   if constexpr (kMma) {
     return columns_mma_launch(a, D, s);
   } else {
-    return run("backward_columns", backward_columns<T, TD, D>,
+    return launch("backward_columns", backward_columns<T, TD, D>,
                dim3((unsigned)(((int64_t)w.segs * a.L + 7) / 8)), 256, 0, s,
                a);
   }
@@ -549,7 +541,7 @@ cudaError_t backward_launch(const BackwardArgs& in, bool bf16, int d, void* ws,
   a.carry = (float*)(p + a.w.carry);
   a.g[0] = (const __nv_bfloat16*)(p + a.w.planes);
   a.g[1] = a.g[0] + a.w.rows * d;
-  // the status area and, behind it, the window maxima
+  // the status area and, behind it, the window maxima and the keys' spans
   cudaError_t e = cudaMemsetAsync(ws, 0, a.w.lows, s);
   if (e != cudaSuccess) return e;
   using bf = __nv_bfloat16;

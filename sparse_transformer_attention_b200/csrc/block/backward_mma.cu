@@ -8,7 +8,6 @@
 // bounds these kernels is reading rows from L2 and issuing instructions, not
 // the tensor pipe; the layouts below keep both low.
 #include "../launch.cuh"
-#include "../profile.cuh"
 #include "backward.cuh"
 
 namespace ca {
@@ -208,6 +207,7 @@ backward_rows_mma(Args a, int ntile) {
   constexpr int KS = D / 16;  // steps of a product over the head dimension
   constexpr int NT = D / 8;   // its 8-wide tiles
   extern __shared__ __align__(16) unsigned char g_smem[];
+  chain();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int gr = lane >> 2, tq = lane & 3;
   const int rg = wid & 3, hf = wid >> 2;  // row group, which half of its work
@@ -751,6 +751,7 @@ backward_columns_mma(Args a, int ntile) {
   constexpr int RS = SM::RS, RC = SM::RC;
   constexpr int KS = D / 16, NT = D / 8;
   extern __shared__ __align__(16) unsigned char g_smem[];
+  chain();
   unsigned char* sK = g_smem;
   unsigned char* sV = sK + SM::keys;
   unsigned char* sB = sV + SM::keys;  // two buffers
@@ -1013,10 +1014,8 @@ cudaError_t rows_as(const Args& a, cudaStream_t s) {
   auto kern = backward_rows_mma<D, NP>;
   cudaError_t e = ensure_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  prof_before(s, "backward_rows");
-  kern<<<(unsigned)ctas, kRowWarps * 32, smem, s>>>(a, ntile);
-  prof_after(s);
-  return cudaGetLastError();
+  return launch("backward_rows", kern, dim3((unsigned)ctas), kRowWarps * 32,
+                smem, s, a, ntile);
 }
 
 template <int D, int NP>
@@ -1027,10 +1026,8 @@ cudaError_t columns_as(const Args& a, cudaStream_t s) {
   auto kern = backward_columns_mma<D, NP>;
   cudaError_t e = ensure_smem(kern, ColSmem<D, NP>::bytes);
   if (e != cudaSuccess) return e;
-  prof_before(s, "backward_columns");
-  kern<<<(unsigned)ctas, kColWarps * 32, ColSmem<D, NP>::bytes, s>>>(a, ntile);
-  prof_after(s);
-  return cudaGetLastError();
+  return launch("backward_columns", kern, dim3((unsigned)ctas),
+                kColWarps * 32, ColSmem<D, NP>::bytes, s, a, ntile);
 }
 
 }  // namespace

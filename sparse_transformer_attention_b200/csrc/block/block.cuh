@@ -8,8 +8,38 @@
 #include <stdint.h>
 
 #include "../common.cuh"
+#include "../profile.cuh"
 
 namespace ca {
+
+// Kernels of one call follow each other by programmatic dependent launch:
+// the next one's CTAs are set up while the last CTAs of the one before run.
+// Every kernel calls chain() before it touches memory; it returns when the
+// kernels before are complete and their writes visible, so the order is that
+// of plain launches.
+__device__ __forceinline__ void chain() {
+  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::
+                   : "memory");
+}
+
+template <typename... P, typename... V>
+cudaError_t launch(const char* name, void (*kern)(P...), dim3 grid,
+                   int threads, size_t smem, cudaStream_t s, V... v) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  prof_before(s, name);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(v)...);
+  prof_after(s);
+  return e;
+}
 
 // N consecutive elements as floats: a multiple of 16 bytes (16-byte aligned),
 // or eight bytes of bf16.

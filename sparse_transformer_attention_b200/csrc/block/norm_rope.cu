@@ -13,7 +13,6 @@
 // elements), a row is 8 to 32 lanes, and four row groups are in flight per
 // lane.  Arithmetic is fp32 with one rounding at the store.
 #include "../launch.cuh"
-#include "../profile.cuh"
 #include "block.cuh"
 
 namespace ca {
@@ -181,6 +180,7 @@ __device__ __forceinline__ void forward_heads(const NormRopeArgs& a,
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32) norm_rope(NormRopeArgs a) {
+  chain();
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int heads = a.Hq + 2 * a.Hkv;
@@ -279,6 +279,7 @@ norm_rope_backward(NormRopeArgs a) {
   using LN = Lanes<T, D>;
   constexpr int EPL = LN::EPL;
   __shared__ float s_dw[kWarps][2][D];
+  chain();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int heads = a.Hq + 2 * a.Hkv;
   const int per = (heads + a.chunk - 1) / a.chunk;
@@ -341,6 +342,7 @@ template <int D>
 __global__ void __launch_bounds__(1024)
 norm_rope_weights(NormRopeArgs a, int ctas) {
   __shared__ float s[32][33];
+  chain();
   const int col = threadIdx.x & 31, part = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + col;
   float x = 0.f;
@@ -383,10 +385,8 @@ cudaError_t forward_as(NormRopeArgs a, cudaStream_t s) {
       (int64_t)a.B * a.n * ((heads + a.chunk - 1) / a.chunk);
   const int64_t ctas = (units + kWarps - 1) / kWarps;
   if (ctas > 0x7FFFFFFF) return cudaErrorNotSupported;
-  prof_before(s, "norm_rope");
-  norm_rope<T, D><<<(unsigned)ctas, kWarps * 32, 0, s>>>(a);
-  prof_after(s);
-  return cudaGetLastError();
+  return launch("norm_rope", norm_rope<T, D>, dim3((unsigned)ctas),
+                kWarps * 32, 0, s, a);
 }
 
 template <typename T, int D>
@@ -398,15 +398,11 @@ cudaError_t backward_as(NormRopeArgs a, cudaStream_t s) {
   int64_t ctas = (units + kWarps - 1) / kWarps;
   if (ctas > kNormRopeMaxCtas) ctas = kNormRopeMaxCtas;
   if (!a.w[0] && !a.w[1]) a.partial = nullptr;
-  prof_before(s, "norm_rope_backward");
-  norm_rope_backward<T, D><<<(unsigned)ctas, kWarps * 32, 0, s>>>(a);
-  prof_after(s);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch("norm_rope_backward", norm_rope_backward<T, D>,
+                               dim3((unsigned)ctas), kWarps * 32, 0, s, a);
   if (e != cudaSuccess || !a.partial) return e;
-  prof_before(s, "norm_rope_weights");
-  norm_rope_weights<D><<<2 * D / 32, 1024, 0, s>>>(a, (int)ctas);
-  prof_after(s);
-  return cudaGetLastError();
+  return launch("norm_rope_weights", norm_rope_weights<D>, dim3(2 * D / 32),
+                1024, 0, s, a, (int)ctas);
 }
 
 }  // namespace

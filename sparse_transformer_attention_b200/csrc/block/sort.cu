@@ -5,9 +5,10 @@
 // places the entries (sort_place), which first orders its tile in shared
 // memory so that what it writes is runs of consecutive places: with entries
 // written where they stood, 32 lanes hit 32 sectors and a pass of the 8K
-// GPT-2-small case took 100 us.
+// GPT-2-small case took 100 us.  Lists of one tile or a few (up to kSmall
+// entries) are sorted by one CTA each in shared memory, in one launch
+// instead of six.
 #include "../launch.cuh"
-#include "../profile.cuh"
 #include "backward.cuh"
 
 namespace ca {
@@ -18,9 +19,16 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSteps = kTile / kThreads;  // entries per thread
 
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallSteps = 16;
+constexpr int kSmall = kSmallThreads * kSmallSteps;
+constexpr size_t kSmallSmem =
+    (size_t)kSmall * 8 + (size_t)(kSmallThreads / 32) * 256 * 2;
+
 __global__ void __launch_bounds__(kThreads)
 sort_count(Args a, const uint32_t* key, int shift, uint32_t mask) {
   __shared__ uint32_t cnt[256];
+  chain();
   const int64_t base = (int64_t)blockIdx.y * a.w.per_head;
   const int64_t e0 = (int64_t)blockIdx.x * kTile;
   const int n = (int)min((int64_t)kTile, a.w.per_head - e0);
@@ -52,9 +60,10 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane) {
 }
 
 // One warp per (kv head, digit): exclusive scan of its counts over the tiles.
-__global__ void __launch_bounds__(kThreads) sort_scan(Args a) {
+__global__ void __launch_bounds__(256) sort_scan(Args a) {
+  chain();
   const int lane = threadIdx.x & 31;
-  const int dg = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int dg = blockIdx.x * 8 + (threadIdx.x >> 5);
   const size_t at = (size_t)blockIdx.y * 256 + dg;
   uint32_t* h = a.hist + at * a.w.tiles;
   uint32_t sum = 0;
@@ -68,24 +77,60 @@ __global__ void __launch_bounds__(kThreads) sort_scan(Args a) {
   if (lane == 0) a.totals[at] = sum;
 }
 
-// Exclusive scan over the CTA's threads.
+// Exclusive scan over the CTA's first 256 threads (the others pass 0).
 __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t* s_warp) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const uint32_t x = warp_scan(v, lane);
-  if (lane == 31) s_warp[wid] = x;
+  if (lane == 31 && wid < 8) s_warp[wid] = x;
   __syncthreads();
   uint32_t before = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w)
+  for (int w = 0; w < 8; ++w)
     if (w < wid) before += s_warp[w];
   __syncthreads();
   return before + x - v;
 }
 
-// Places a tile.  Every warp ranks its run of the tile's entries in order
-// (equal digits of a step by lane, earlier steps by a running count), the
-// warps' counts are chained, and the tile, ordered by digit in shared
-// memory, goes out run by run.
+// The lanes of the warp with this lane's digit (one vote per digit bit; a
+// vote takes a few cycles where match.any takes one round per value).
+__device__ __forceinline__ uint32_t peers(uint32_t dg, int bits) {
+  uint32_t same = kAll;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (i < bits) {
+      const uint32_t set = __ballot_sync(kAll, (dg >> i) & 1u);
+      same &= ((dg >> i) & 1u) ? set : ~set;
+    }
+  }
+  return same;
+}
+
+// Ranks a warp's run of STEPS x 32 entries in order: equal digits of a step
+// by lane, earlier steps by the running counts cnt[256].  Entries behind the
+// end (live 0) are a tail of the run.
+template <int STEPS>
+__device__ __forceinline__ void rank_run(const uint32_t (&kv)[STEPS],
+                                         uint32_t (&rank)[STEPS], int live,
+                                         int shift, uint32_t mask, int bits,
+                                         uint16_t* cnt) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int u = 0; u < STEPS; ++u) {
+    const bool in = u * 32 + lane < live;
+    const uint32_t dg = (kv[u] >> shift) & mask;
+    const uint32_t same = peers(dg, bits) & __ballot_sync(kAll, in);
+    const uint32_t lower = same & ((1u << lane) - 1u);
+    uint32_t before = 0;
+    if (in) before = cnt[dg];
+    __syncwarp();
+    if (in && lower == 0) cnt[dg] = (uint16_t)(before + __popc(same));
+    __syncwarp();
+    rank[u] = before + __popc(lower);
+  }
+}
+
+// Places a tile: the warps' runs are ranked, their counts chained, and the
+// tile, ordered by digit in shared memory, goes out run by run.
 __global__ void __launch_bounds__(kThreads, 2)
 sort_place(Args a, const uint32_t* key, const uint32_t* ent, uint32_t* key_out,
            uint32_t* ent_out, int shift, uint32_t mask) {
@@ -93,14 +138,13 @@ sort_place(Args a, const uint32_t* key, const uint32_t* ent, uint32_t* key_out,
   __shared__ uint32_t s_key[kTile], s_ent[kTile];
   __shared__ uint32_t s_dst[256];  // global place of the tile's run, less its
                                    // local place
-  __shared__ uint32_t s_warp[kWarps];
+  __shared__ uint32_t s_warp[8];
+  chain();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int64_t base = (int64_t)blockIdx.y * a.w.per_head;
   const int64_t t0 = (int64_t)blockIdx.x * kTile;
   const int n = (int)min((int64_t)kTile, a.w.per_head - t0);
   const int l0 = wid * (32 * kSteps);
-  for (int c = threadIdx.x; c < kWarps * 256; c += kThreads)
-    (&cnt[0][0])[c] = 0;
   uint32_t kv[kSteps], ev[kSteps], rank[kSteps];
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
@@ -108,34 +152,25 @@ sort_place(Args a, const uint32_t* key, const uint32_t* ent, uint32_t* key_out,
     kv[u] = l < n ? key[base + t0 + l] : 0u;
     ev[u] = ent && l < n ? ent[base + t0 + l] : (uint32_t)(t0 + l);
   }
+  const int dg = threadIdx.x;  // one digit per thread of the first 256
+  const bool mine = dg < 256;
+  const size_t at_dg = (size_t)blockIdx.y * 256 + (mine ? dg : 0);
+  const uint32_t all = mine ? a.totals[at_dg] : 0u;
+  const uint32_t prior = a.hist[at_dg * a.w.tiles + blockIdx.x];
+  for (int c = threadIdx.x; c < kWarps * 256; c += kThreads)
+    (&cnt[0][0])[c] = 0;
   __syncthreads();
-#pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const bool live = l0 + u * 32 + lane < n;
-    // lanes behind the tile's end share a digit that no other lane has
-    const uint32_t dg = live ? (kv[u] >> shift) & mask : 256u;
-    const uint32_t same = __match_any_sync(kAll, dg);
-    const uint32_t lower = same & ((1u << lane) - 1u);
-    uint32_t before = 0;
-    if (live) before = cnt[wid][dg];
-    __syncwarp();
-    if (live && lower == 0) cnt[wid][dg] = (uint16_t)(before + __popc(same));
-    __syncwarp();
-    rank[u] = before + __popc(lower);
-  }
+  rank_run<kSteps>(kv, rank, n - l0, shift, mask, a.w.digit, cnt[wid]);
   __syncthreads();
   {
-    const int dg = threadIdx.x;  // one digit per thread of the first 256
-    const bool mine = dg < 256;
-    const size_t at = (size_t)blockIdx.y * 256 + (mine ? dg : 0);
     uint32_t total = 0;
     if (mine)
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) total += cnt[w][dg];
     const uint32_t local = cta_scan(total, s_warp);
-    const uint32_t first = cta_scan(mine ? a.totals[at] : 0u, s_warp);
+    const uint32_t first = cta_scan(all, s_warp);
     if (mine) {
-      s_dst[dg] = first + a.hist[at * a.w.tiles + blockIdx.x] - local;
+      s_dst[dg] = first + prior - local;
       uint32_t x = local;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
@@ -171,28 +206,106 @@ sort_place(Args a, const uint32_t* key, const uint32_t* ent, uint32_t* key_out,
   }
 }
 
+// All passes over one kv head's list, one CTA, the list in shared memory.
+__global__ void __launch_bounds__(kSmallThreads)
+sort_small(Args a, const uint32_t* key, uint32_t* key_out, uint32_t* ent_out) {
+  constexpr int kW = kSmallThreads / 32;
+  extern __shared__ __align__(16) unsigned char g_smem[];
+  __shared__ uint32_t s_warp[8];
+  chain();
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(g_smem);
+  uint32_t* s_ent = s_key + kSmall;
+  uint16_t(*cnt)[256] = reinterpret_cast<uint16_t(*)[256]>(s_ent + kSmall);
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int64_t base = (int64_t)blockIdx.x * a.w.per_head;
+  const int n = (int)a.w.per_head;
+  // a warp's run: as many steps as the list needs
+  const int steps = (n + kSmallThreads - 1) / kSmallThreads;
+  const int l0 = wid * 32 * steps;
+  const uint32_t mask = (1u << a.w.digit) - 1u;
+  uint32_t kv[kSmallSteps], ev[kSmallSteps], rank[kSmallSteps];
+#pragma unroll
+  for (int u = 0; u < kSmallSteps; ++u) {
+    const int l = l0 + u * 32 + lane;
+    kv[u] = u < steps && l < n ? key[base + l] : 0u;
+    ev[u] = (uint32_t)l;
+  }
+  for (int p = 0; p < a.w.passes; ++p) {
+    const int shift = p * a.w.digit;
+    for (int c = threadIdx.x; c < kW * 256; c += kSmallThreads)
+      (&cnt[0][0])[c] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kSmallSteps; ++u)
+      if (u < steps) {
+        uint32_t k1[1] = {kv[u]}, r1[1];
+        rank_run<1>(k1, r1, n - l0 - u * 32, shift, mask, a.w.digit, cnt[wid]);
+        rank[u] = r1[0];
+      }
+    __syncthreads();
+    const int dg = threadIdx.x;
+    uint32_t total = 0;
+    if (dg < 256)
+      for (int w = 0; w < kW; ++w) total += cnt[w][dg];
+    uint32_t x = cta_scan(total, s_warp);
+    if (dg < 256)
+      for (int w = 0; w < kW; ++w) {
+        const uint32_t c = cnt[w][dg];
+        cnt[w][dg] = (uint16_t)x;
+        x += c;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kSmallSteps; ++u)
+      if (u < steps && l0 + u * 32 + lane < n) {
+        const uint32_t at = cnt[wid][(kv[u] >> shift) & mask] + rank[u];
+        if (in_bounds(at < (uint32_t)kSmall, a.status)) {
+          s_key[at] = kv[u];
+          s_ent[at] = ev[u];
+        }
+      }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kSmallSteps; ++u) {
+      const int l = l0 + u * 32 + lane;
+      if (u < steps && l < n) {
+        kv[u] = s_key[l];
+        ev[u] = s_ent[l];
+      }
+    }
+  }
+  for (int l = threadIdx.x; l < n; l += kSmallThreads) {
+    key_out[base + l] = s_key[l];
+    ent_out[base + l] = s_ent[l];
+  }
+}
+
 }  // namespace
 
 cudaError_t sort_launch(const Args& a, int* last, cudaStream_t s) {
   const Work& w = a.w;
+  if (w.per_head <= kSmall) {
+    static_assert(kSmall <= 65536, "places fit 16 bits");
+    const cudaError_t e = ensure_smem(sort_small, kSmallSmem);
+    if (e != cudaSuccess) return e;
+    *last = 1;
+    return launch("sort_small", sort_small, dim3(w.segs), kSmallThreads,
+                  kSmallSmem, s, a, a.key[0], a.key[1], a.ent[1]);
+  }
   const dim3 grid(w.tiles, w.segs);
   int from = 0;
   for (int p = 0; p < w.passes; ++p) {
     const int shift = p * w.digit;
     const uint32_t mask = (1u << w.digit) - 1u;
-    prof_before(s, "sort_count");
-    sort_count<<<grid, kThreads, 0, s>>>(a, a.key[from], shift, mask);
-    prof_after(s);
-    prof_before(s, "sort_scan");
-    sort_scan<<<dim3(256 / kWarps, w.segs), kThreads, 0, s>>>(a);
-    prof_after(s);
-    prof_before(s, "sort_place");
-    sort_place<<<grid, kThreads, 0, s>>>(a, a.key[from],
-                                         p ? a.ent[from] : nullptr,
-                                         a.key[from ^ 1], a.ent[from ^ 1],
-                                         shift, mask);
-    prof_after(s);
-    const cudaError_t e = cudaGetLastError();
+    const uint32_t* ent = p ? a.ent[from] : nullptr;
+    cudaError_t e = launch("sort_count", sort_count, grid, kThreads, 0, s, a,
+                           a.key[from], shift, mask);
+    if (e == cudaSuccess)
+      e = launch("sort_scan", sort_scan, dim3(32, w.segs), 256, 0, s, a);
+    if (e == cudaSuccess)
+      e = launch("sort_place", sort_place, grid, kThreads, 0, s, a,
+                 a.key[from], ent, a.key[from ^ 1], a.ent[from ^ 1], shift,
+                 mask);
     if (e != cudaSuccess) return e;
     from ^= 1;
   }
