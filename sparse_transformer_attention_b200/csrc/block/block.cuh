@@ -107,7 +107,6 @@ struct NormRopeArgs {
   int pos0;
   float* partial;       // backward: [CTAs, 2, d] weight-gradient partials
   void* dw[2];          // backward: [d] weight gradients
-  int chunk;            // heads per warp (set by the launcher)
 };
 
 // CTAs of the backward pass at most (they keep weight-gradient sums in

@@ -5,13 +5,18 @@
 //   y = x * rsqrt(mean(x^2) + eps) * w          (rows with a norm weight)
 //   (a, b) -> (a cos - b sin, b cos + a sin)    angle = position * inv_freq
 //
-// Both are bound by HBM: every row is read once and written once.  A warp
-// owns one token (or some of its heads, when there are few tokens), so the
-// angles of that token are computed once, one or two pairs per lane, handed
-// round by shuffles and kept in registers for all its heads: no table is
-// read and no shared memory used.  A lane holds 16 bytes of a row (4 or 8
-// elements), a row is 8 to 32 lanes, and four row groups are in flight per
-// lane.  Arithmetic is fp32 with one rounding at the store.
+// Both are bound by HBM: every row is read once and written once.  A CTA
+// owns a tile of 1 to 16 tokens.  It computes the tile's angles once, as a
+// table of cos and sin per element in shared memory (every head of a token
+// shares them; elements that are not rotated have cos 1, sin 0), and its
+// warps walk over the tile's rows, tokens fastest, so that what a warp
+// writes of a head is contiguous.  A lane holds 16 bytes of a row (4 or 8
+// elements), a row is 8 to 32 lanes, and the rows of several steps are on
+// their way at a time.  Arithmetic is fp32 with one rounding at the store.
+//
+// A warp per token with its angles in registers was 94 us where this is 62
+// (GPT-2-small shape, 4 x 8192 tokens): the angles' registers held it at 16
+// warps per SM, and the first rows of q, k and v each waited out a latency.
 #include "../launch.cuh"
 #include "block.cuh"
 
@@ -19,6 +24,8 @@ namespace ca {
 namespace {
 
 constexpr int kWarps = 8;  // per CTA
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxTile = 16;  // tokens
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // cos and sin of position * inv_freq.  The product is taken in 64 bits and
@@ -32,73 +39,56 @@ __device__ __forceinline__ void angle(int pos, float inv_freq, float* c,
   sincospif(2.f * (float)turns, s, c);
 }
 
-// The EPL = 16 / sizeof(T) elements per lane of a row and what rotates them.
+// Two fp32 values in one 64-bit register, for the packed arithmetic that
+// halves the instructions of what is otherwise bound by issuing them.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 both(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// 16 bytes of a row as pairs, and back (rounded to nearest even once).
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const uint4& in, F2 (&v)[N]) {
+  float f[2 * N];
+  Elem<T>::unpack(in, f);
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
+}
+template <typename T, int N>
+__device__ __forceinline__ uint4 pack(const F2 (&v)[N]) {
+  float f[2 * N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float2 x = both(v[e]);
+    f[2 * e] = x.x;
+    f[2 * e + 1] = x.y;
+  }
+  return pack16<T>(f);
+}
+
 template <typename T, int D>
 struct Lanes {
-  static constexpr int EPL = Elem<T>::kPer16B;
-  static constexpr int LPR = D / EPL;   // lanes per row
-  static constexpr int RW = 32 / LPR;   // rows per warp and step
-  int sub;        // this lane's place in its row
-  int src;        // lane that holds the partners (split pairs)
-  bool turns;     // whether this lane's elements are rotated
-  float c[EPL], s[EPL];  // cos; sin with the sign of the element's place
-
-  __device__ __forceinline__ void init(const NormRopeArgs& a, int lane) {
-    sub = lane % LPR;
-    const int half = a.rot / 2 / EPL;  // lanes of a half row (split pairs)
-    turns = sub * EPL < a.rot;
-    src = lane;
-    if (!a.interleaved && turns) src = sub < half ? lane + half : lane - half;
-  }
-
-  // The angles of one token, with sign +1 for the rotation and -1 for its
-  // transpose.
-  __device__ __forceinline__ void set_token(const NormRopeArgs& a, int pos,
-                                            int lane, float sign) {
-    constexpr int NP = D / 2 / 32;  // pairs per lane: 1 or 2
-    const int pairs = a.rot / 2;
-    float pc[NP], ps[NP];
-#pragma unroll
-    for (int u = 0; u < NP; ++u) {
-      const int p = lane + 32 * u;
-      pc[u] = 1.f;
-      ps[u] = 0.f;
-      if (p < pairs) angle(pos, __ldg(a.inv_freq + p), &pc[u], &ps[u]);
-    }
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) {
-      const int el = sub * EPL + e;
-      int p = a.interleaved ? el / 2 : (el < pairs ? el : el - pairs);
-      const bool first = a.interleaved ? (e & 1) == 0 : el < pairs;
-      if (!turns) p = 0;
-      float cc = __shfl_sync(kAll, pc[0], p & 31);
-      float ss = __shfl_sync(kAll, ps[0], p & 31);
-      if constexpr (NP == 2) {
-        const float c1 = __shfl_sync(kAll, pc[1], p & 31);
-        const float s1 = __shfl_sync(kAll, ps[1], p & 31);
-        if (p >= 32) {
-          cc = c1;
-          ss = s1;
-        }
-      }
-      c[e] = turns ? cc : 1.f;
-      s[e] = turns ? (first ? -sign * ss : sign * ss) : 0.f;
-    }
-  }
-
-  // The rotation of one row (every lane of the warp takes part).
-  __device__ __forceinline__ void rotate(bool interleaved, float* v) const {
-    float o[EPL];
-    if (interleaved) {
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) o[e] = v[e ^ 1];
-    } else {
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) o[e] = __shfl_sync(kAll, v[e], src);
-    }
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) v[e] = fmaf(v[e], c[e], o[e] * s[e]);
-  }
+  static constexpr int EPL = Elem<T>::kPer16B;  // elements per lane
+  static constexpr int NP = EPL / 2;            // pairs of them
+  static constexpr int LPR = D / EPL;           // lanes per row
+  static constexpr int RW = 32 / LPR;           // rows per warp and step
 
   __device__ __forceinline__ static float row_sum(float x) {
 #pragma unroll
@@ -106,229 +96,311 @@ struct Lanes {
       x += __shfl_xor_sync(kAll, x, off);
     return x;
   }
-
-  __device__ __forceinline__ void weights(const void* w, int bf16,
-                                          float* f) const {
+  __device__ __forceinline__ static void weights(const void* w, int bf16,
+                                                 int el, F2 (&f)[NP]) {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e)
-      f[e] = bf16 ? __bfloat162float(
-                        reinterpret_cast<const __nv_bfloat16*>(w)[sub * EPL + e])
-                  : reinterpret_cast<const float*>(w)[sub * EPL + e];
+    for (int e = 0; e < NP; ++e) {
+      float2 v;
+      if (bf16) {
+        const __nv_bfloat16* p =
+            reinterpret_cast<const __nv_bfloat16*>(w) + el + 2 * e;
+        v = make_float2(__bfloat162float(p[0]), __bfloat162float(p[1]));
+      } else {
+        const float* p = reinterpret_cast<const float*>(w) + el + 2 * e;
+        v = make_float2(p[0], p[1]);
+      }
+      f[e] = pair(v.x, v.y);
+    }
   }
 };
 
-template <typename T>
-__device__ __forceinline__ const uint4* row_at(const Rows& r, int b, int t,
-                                               int h, int el) {
-  return reinterpret_cast<const uint4*>(
-      reinterpret_cast<const T*>(r.p) + b * r.sb + t * r.st + h * r.sh + el);
-}
-template <typename T>
-__device__ __forceinline__ uint4* row_to(const Rows& r, int b, int t, int h,
-                                         int el) {
-  return reinterpret_cast<uint4*>(reinterpret_cast<T*>(r.p) + b * r.sb +
-                                  t * r.st + h * r.sh + el);
+// A tile's angles and row offsets.  cs holds cos, then sin with the sign of
+// the element's place (first of a pair: minus), in pieces of four elements
+// laid out so that neighbouring lanes read neighbouring 16 bytes.
+template <typename T, int D>
+struct Tile {
+  using LN = Lanes<T, D>;
+  static constexpr int NQ = LN::EPL / 4;  // pieces per lane
+  alignas(16) float cs[kMaxTile][2][NQ][LN::LPR][4];
+  int64_t off[9][kMaxTile];  // row offsets in x, y and dx of q, k, v
+
+  __device__ __forceinline__ void offsets(const NormRopeArgs& a,
+                                          int64_t token0, int count,
+                                          bool grad) {
+    for (int t = threadIdx.x; t < count; t += kThreads) {
+      const int64_t b = (token0 + t) / a.n, tt = (token0 + t) % a.n;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        off[k][t] = b * a.x[k].sb + tt * a.x[k].st;
+        off[3 + k][t] = b * a.y[k].sb + tt * a.y[k].st;
+        if (grad) off[6 + k][t] = b * a.dx[k].sb + tt * a.dx[k].st;
+      }
+    }
+  }
+  // sign: +1 for the rotation, -1 for its transpose.
+  __device__ __forceinline__ void fill(const NormRopeArgs& a, int64_t token0,
+                                       int count, float sign) {
+    const int half = a.rot / 2;
+    for (int e = threadIdx.x; e < count * (D / 2); e += kThreads) {
+      const int t = e / (D / 2), p = e % (D / 2);
+      const int64_t token = token0 + t;
+      // pair p: elements (lo, hi); behind the rotated part, two plain ones
+      int lo = 2 * p, hi = 2 * p + 1;
+      float c = 1.f, s = 0.f;
+      if (p < half) {
+        if (!a.interleaved) {
+          lo = p;
+          hi = p + half;
+        }
+        const int pos = a.positions ? a.positions[token]
+                                    : a.pos0 + (int)(token % a.n);
+        angle(pos, __ldg(a.inv_freq + p), &c, &s);
+      }
+      at(t, 0, lo) = c;
+      at(t, 0, hi) = c;
+      at(t, 1, lo) = -sign * s;
+      at(t, 1, hi) = sign * s;
+    }
+  }
+  __device__ __forceinline__ float& at(int t, int k, int el) {
+    return cs[t][k][el % LN::EPL / 4][el / LN::EPL][el % 4];
+  }
+  __device__ __forceinline__ void load(int t, int k, int sub,
+                                       F2 (&f)[LN::NP]) const {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const ulonglong2 v =
+          *reinterpret_cast<const ulonglong2*>(cs[t][k][q][sub]);
+      f[2 * q] = v.x;
+      f[2 * q + 1] = v.y;
+    }
+  }
+  // v turned by the angles of tile token t.  src: the lane that holds the
+  // partners of split pairs.
+  __device__ __forceinline__ void rotate(int t, int sub, int src,
+                                         bool interleaved,
+                                         F2 (&v)[LN::NP]) const {
+    F2 o[LN::NP], c[LN::NP];
+#pragma unroll
+    for (int e = 0; e < LN::NP; ++e) {
+      const float2 x = both(v[e]);
+      o[e] = interleaved ? pair(x.y, x.x)
+                         : pair(__shfl_sync(kAll, x.x, src),
+                                __shfl_sync(kAll, x.y, src));
+    }
+    load(t, 0, sub, c);
+#pragma unroll
+    for (int e = 0; e < LN::NP; ++e) v[e] = mul(v[e], c[e]);
+    load(t, 1, sub, c);
+#pragma unroll
+    for (int e = 0; e < LN::NP; ++e) v[e] = fma(o[e], c[e], v[e]);
+  }
+};
+
+// This lane's place in its row and the lane of its partners (itself behind
+// the rotated part).
+template <typename T, int D>
+__device__ __forceinline__ int partner(const NormRopeArgs& a, int lane) {
+  using LN = Lanes<T, D>;
+  const int sub = lane % LN::LPR, half = a.rot / 2 / LN::EPL;
+  if (a.interleaved || sub * LN::EPL >= a.rot) return lane;
+  return sub < half ? lane + half : lane - half;
 }
 
-// Heads [h0, h1) of one kind (0 q, 1 k, 2 v) of one token.
-template <typename T, int D, int U>
-__device__ __forceinline__ void forward_heads(const NormRopeArgs& a,
-                                              const Lanes<T, D>& L, int kind,
-                                              int b, int t, int h0, int h1,
-                                              int lane) {
+template <typename T>
+__device__ __forceinline__ uint4* row_at(const Rows& r, int64_t off, int h) {
+  return reinterpret_cast<uint4*>(reinterpret_cast<T*>(r.p) + off + h * r.sh);
+}
+
+// The rows of one kind (0 q, 1 k, 2 v) of the tile: H heads of 1 << lt
+// tokens, of which `count` exist.
+template <typename T, int D, int KIND>
+__device__ __forceinline__ void forward_rows(const NormRopeArgs& a,
+                                             const Tile<T, D>& tile, int lt,
+                                             int count, int H) {
   using LN = Lanes<T, D>;
-  constexpr int EPL = LN::EPL;
-  const Rows x = a.x[kind], y = a.y[kind];
-  const bool norm = kind < 2 && a.w[kind];
-  float w[EPL];
-  if (norm) L.weights(a.w[kind], a.w_bf16, w);
-  const int el = L.sub * EPL;
+  constexpr int EPL = LN::EPL, NP = LN::NP, U = 4;  // U steps on their way
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int sub = lane % LN::LPR, src = partner<T, D>(a, lane);
+  const Rows x = a.x[KIND], y = a.y[KIND];
+  const bool norm = KIND < 2 && a.w[KIND < 2 ? KIND : 0];
+  F2 w[NP];
+  if (norm) LN::weights(a.w[KIND < 2 ? KIND : 0], a.w_bf16, sub * EPL, w);
+  const int rows = H << lt, tm = (1 << lt) - 1;
+  constexpr int kStep = kWarps * LN::RW;
 #pragma unroll 1
-  for (int h = h0 + lane / LN::LPR; h - lane / LN::LPR < h1;
-       h += U * LN::RW) {
+  for (int r0 = wid * LN::RW; r0 < rows; r0 += U * kStep) {
+    const int r = r0 + lane / LN::LPR;
     uint4 in[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      const int ru = r + u * kStep, t = ru & tm;
       in[u] = make_uint4(0, 0, 0, 0);
-      if (h + u * LN::RW < h1)
-        in[u] = __ldg(row_at<T>(x, b, t, h + u * LN::RW, el));
+      if (ru < rows && t < count)
+        in[u] = __ldg(row_at<T>(x, tile.off[KIND][t] + sub * EPL, ru >> lt));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int hu = h + u * LN::RW;
-      if (hu - lane / LN::LPR >= h1) break;  // uniform over the warp
+      const int ru = r + u * kStep, t = ru & tm;
+      if (r0 + u * kStep >= rows) break;  // the same for the warp
       uint4 out = in[u];
-      if (kind < 2) {
-        float v[EPL];
-        Elem<T>::unpack(in[u], v);
+      if (KIND < 2) {
+        F2 v[NP];
+        unpack<T>(out, v);
         if (norm) {
-          float ss = 0.f;
+          F2 s2 = mul(v[0], v[0]);
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) ss = fmaf(v[e], v[e], ss);
-          ss = LN::row_sum(ss);
-          const float r = rsqrtf(ss * (1.f / D) + a.eps);
+          for (int e = 1; e < NP; ++e) s2 = fma(v[e], v[e], s2);
+          const float2 ss = both(s2);
+          const float q =
+              rsqrtf(LN::row_sum(ss.x + ss.y) * (1.f / D) + a.eps);
+          const F2 q2 = pair(q, q);
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) v[e] *= r * w[e];
+          for (int e = 0; e < NP; ++e) v[e] = mul(v[e], mul(w[e], q2));
         }
-        L.rotate(a.interleaved, v);
-        out = pack16<T>(v);
+        tile.rotate(t, sub, src, a.interleaved, v);
+        out = pack<T>(v);
       }
-      if (hu < h1) *row_to<T>(y, b, t, hu, el) = out;
+      if (ru < rows && t < count)
+        *row_at<T>(y, tile.off[3 + KIND][t] + sub * EPL, ru >> lt) = out;
     }
   }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) norm_rope(NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 4)
+norm_rope(NormRopeArgs a, int lt) {
+  __shared__ Tile<T, D> tile;
   chain();
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int per = (heads + a.chunk - 1) / a.chunk;  // warps per token
-  const int64_t token = unit / per;
-  if (token >= (int64_t)a.B * a.n) return;  // the whole warp
-  const int c0 = (int)(unit % per) * a.chunk;
-  const int c1 = min(c0 + a.chunk, heads);
-  const int b = (int)(token / a.n), t = (int)(token % a.n);
-  Lanes<T, D> L;
-  L.init(a, lane);
-  if (c0 < a.Hq + a.Hkv)
-    L.set_token(a, a.positions ? a.positions[token] : a.pos0 + t, lane, 1.f);
-#pragma unroll 1
-  for (int kind = 0; kind < 3; ++kind) {
-    const int k0 = kind == 0 ? 0 : a.Hq + (kind - 1) * a.Hkv;
-    const int nh = kind == 0 ? a.Hq : a.Hkv;
-    const int h0 = max(c0 - k0, 0), h1 = min(c1 - k0, nh);
-    if (h0 < h1 && a.y[kind].p)
-      forward_heads<T, D, 4>(a, L, kind, b, t, h0, h1, lane);
-  }
+  const int64_t tokens = (int64_t)a.B * a.n;
+  const int64_t t0 = (int64_t)blockIdx.x << lt;
+  const int count = (int)min((int64_t)1 << lt, tokens - t0);
+  tile.offsets(a, t0, count, false);
+  tile.fill(a, t0, count, 1.f);
+  __syncthreads();
+  forward_rows<T, D, 0>(a, tile, lt, count, a.Hq);
+  if (a.y[1].p) forward_rows<T, D, 1>(a, tile, lt, count, a.Hkv);
+  if (a.y[2].p) forward_rows<T, D, 2>(a, tile, lt, count, a.Hkv);
 }
 
-// dx of one head row, and its part of the weight's gradient:
+// Gradients of one kind's rows, and their part of the weight's gradient:
 //   g = R^T dy,  xh = x r,  dw += g xh,
 //   dx = r (w g - xh mean(w g xh))
-template <typename T, int D, int U>
-__device__ __forceinline__ void backward_heads(const NormRopeArgs& a,
-                                               const Lanes<T, D>& L, int kind,
-                                               int b, int t, int h0, int h1,
-                                               int lane, float* dw) {
+template <typename T, int D, int KIND>
+__device__ __forceinline__ void backward_rows(const NormRopeArgs& a,
+                                              const Tile<T, D>& tile, int lt,
+                                              int count, int H,
+                                              F2* dw) {
   using LN = Lanes<T, D>;
-  constexpr int EPL = LN::EPL;
-  const Rows x = a.x[kind], y = a.y[kind], dx = a.dx[kind];
-  const bool norm = kind < 2 && a.w[kind];
-  float w[EPL];
-  if (norm) L.weights(a.w[kind], a.w_bf16, w);
-  const int el = L.sub * EPL;
+  constexpr int EPL = LN::EPL, NP = LN::NP;
+  constexpr int U = KIND < 2 ? 4 : 4;  // steps on their way
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int sub = lane % LN::LPR, src = partner<T, D>(a, lane);
+  const Rows x = a.x[KIND], y = a.y[KIND], dx = a.dx[KIND];
+  const bool norm = KIND < 2 && a.w[KIND < 2 ? KIND : 0];
+  F2 w[NP];
+  if (norm) LN::weights(a.w[KIND < 2 ? KIND : 0], a.w_bf16, sub * EPL, w);
+  const int rows = H << lt, tm = (1 << lt) - 1;
+  constexpr int kStep = kWarps * LN::RW;
 #pragma unroll 1
-  for (int h = h0 + lane / LN::LPR; h - lane / LN::LPR < h1;
-       h += U * LN::RW) {
+  for (int r0 = wid * LN::RW; r0 < rows; r0 += U * kStep) {
+    const int r = r0 + lane / LN::LPR;
     uint4 in[U], xin[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      in[u] = make_uint4(0, 0, 0, 0);
-      xin[u] = make_uint4(0, 0, 0, 0);
-      if (h + u * LN::RW < h1) {
-        in[u] = __ldg(row_at<T>(y, b, t, h + u * LN::RW, el));
-        if (norm) xin[u] = __ldg(row_at<T>(x, b, t, h + u * LN::RW, el));
+      const int ru = r + u * kStep, t = ru & tm;
+      in[u] = xin[u] = make_uint4(0, 0, 0, 0);
+      if (ru < rows && t < count) {
+        in[u] = __ldg(row_at<T>(y, tile.off[3 + KIND][t] + sub * EPL, ru >> lt));
+        if (norm)
+          xin[u] =
+              __ldg(row_at<T>(x, tile.off[KIND][t] + sub * EPL, ru >> lt));
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int hu = h + u * LN::RW;
-      if (hu - lane / LN::LPR >= h1) break;  // uniform over the warp
+      const int ru = r + u * kStep, t = ru & tm;
+      if (r0 + u * kStep >= rows) break;  // the same for the warp
       uint4 out = in[u];
-      if (kind < 2) {
-        float g[EPL];
-        Elem<T>::unpack(in[u], g);
-        L.rotate(a.interleaved, g);
+      if (KIND < 2) {
+        F2 g[NP];
+        unpack<T>(out, g);
+        tile.rotate(t, sub, src, a.interleaved, g);
         if (norm) {
-          float v[EPL];
-          Elem<T>::unpack(xin[u], v);
-          float ss = 0.f, dot = 0.f;
+          F2 v[NP], gv[NP];
+          unpack<T>(xin[u], v);
+          F2 s2 = mul(v[0], v[0]), d2;
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) {
-            ss = fmaf(v[e], v[e], ss);
-            dot = fmaf(g[e] * w[e], v[e], dot);
+          for (int e = 0; e < NP; ++e) {
+            gv[e] = mul(g[e], v[e]);
+            if (e > 0) s2 = fma(v[e], v[e], s2);
+            d2 = e > 0 ? fma(gv[e], w[e], d2) : mul(gv[e], w[e]);
           }
-          ss = LN::row_sum(ss);
-          dot = LN::row_sum(dot);
-          const float r = rsqrtf(ss * (1.f / D) + a.eps);
-          const float m = dot * r * (1.f / D);  // mean(w g xh)
+          const float2 ss = both(s2), dd = both(d2);
+          const float q =
+              rsqrtf(LN::row_sum(ss.x + ss.y) * (1.f / D) + a.eps);
+          // r^2 mean(w g xh), the part of dx along x
+          const float m =
+              LN::row_sum(dd.x + dd.y) * (1.f / D) * (q * q * q);
+          const F2 q2 = pair(q, q), m2 = pair(-m, -m);
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) {
-            const float xh = v[e] * r;
-            dw[e] = fmaf(g[e], xh, dw[e]);  // rows past h1 hold zeros
-            g[e] = r * (g[e] * w[e] - xh * m);
+          for (int e = 0; e < NP; ++e) {
+            dw[e] = fma(gv[e], q2, dw[e]);  // absent rows hold zeros
+            g[e] = fma(m2, v[e], mul(g[e], mul(w[e], q2)));
           }
         }
-        out = pack16<T>(g);
+        out = pack<T>(g);
       }
-      if (hu < h1) *row_to<T>(dx, b, t, hu, el) = out;
+      if (ru < rows && t < count)
+        *row_at<T>(dx, tile.off[6 + KIND][t] + sub * EPL, ru >> lt) = out;
     }
   }
 }
 
-// A CTA's warps walk over the tokens with a stride; each lane sums the
-// weight gradients of its elements over all rows it sees (q and k apart).
-// At the end the sums meet in a fixed order: over the row groups of a warp,
-// over the warps, and over the CTAs (norm_rope_weights), so a result does
-// not depend on timing.
+// A CTA's tiles follow each other with a stride of the grid; each lane sums
+// the weight gradients of its elements over all rows it sees (q and k
+// apart).  At the end the sums meet in a fixed order: over the rows of a
+// warp's step, over the warps, and over the CTAs (norm_rope_weights), so a
+// result does not depend on timing.
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
-norm_rope_backward(NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 2)
+norm_rope_backward(NormRopeArgs a, int lt) {
   using LN = Lanes<T, D>;
   constexpr int EPL = LN::EPL;
+  __shared__ Tile<T, D> tile;
   __shared__ float s_dw[kWarps][2][D];
   chain();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int per = (heads + a.chunk - 1) / a.chunk;
-  const int64_t units = (int64_t)a.B * a.n * per;
-  float dw[2][EPL];
+  const int64_t tokens = (int64_t)a.B * a.n;
+  F2 dw[2][LN::NP];
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) dw[0][e] = dw[1][e] = 0.f;
-  LN L;
-  L.init(a, lane);
+  for (int e = 0; e < LN::NP; ++e) dw[0][e] = dw[1][e] = 0;
 #pragma unroll 1
-  for (int64_t unit = (int64_t)blockIdx.x * kWarps + wid; unit < units;
-       unit += (int64_t)gridDim.x * kWarps) {
-    const int64_t token = unit / per;
-    const int c0 = (int)(unit % per) * a.chunk;
-    const int c1 = min(c0 + a.chunk, heads);
-    const int b = (int)(token / a.n), t = (int)(token % a.n);
-    if (c0 < a.Hq + a.Hkv)
-      L.set_token(a, a.positions ? a.positions[token] : a.pos0 + t, lane,
-                  -1.f);
-    {
-      const int h1 = min(c1, a.Hq);
-      if (c0 < h1)
-        backward_heads<T, D, 2>(a, L, 0, b, t, c0, h1, lane, dw[0]);
-    }
-    {
-      const int h0 = max(c0 - a.Hq, 0), h1 = min(c1 - a.Hq, a.Hkv);
-      if (h0 < h1 && a.dx[1].p)
-        backward_heads<T, D, 2>(a, L, 1, b, t, h0, h1, lane, dw[1]);
-    }
-    {
-      const int k0 = a.Hq + a.Hkv;
-      const int h0 = max(c0 - k0, 0), h1 = min(c1 - k0, a.Hkv);
-      if (h0 < h1 && a.dx[2].p)
-        backward_heads<T, D, 4>(a, L, 2, b, t, h0, h1, lane, nullptr);
-    }
+  for (int64_t t0 = (int64_t)blockIdx.x << lt; t0 < tokens;
+       t0 += (int64_t)gridDim.x << lt) {
+    const int count = (int)min((int64_t)1 << lt, tokens - t0);
+    tile.offsets(a, t0, count, true);
+    tile.fill(a, t0, count, -1.f);
+    __syncthreads();
+    backward_rows<T, D, 0>(a, tile, lt, count, a.Hq, dw[0]);
+    if (a.dx[1].p) backward_rows<T, D, 1>(a, tile, lt, count, a.Hkv, dw[1]);
+    if (a.dx[2].p) backward_rows<T, D, 2>(a, tile, lt, count, a.Hkv, nullptr);
+    __syncthreads();  // the tile's table has been read
   }
   if (!a.partial) return;
 #pragma unroll
   for (int kd = 0; kd < 2; ++kd)
 #pragma unroll
     for (int e = 0; e < EPL; ++e) {
-      float x = dw[kd][e];
+      const float2 p = both(dw[kd][e / 2]);
+      float x = (e & 1) ? p.y : p.x;
 #pragma unroll
       for (int off = 16; off >= LN::LPR; off >>= 1)
         x += __shfl_xor_sync(kAll, x, off);
       if (lane < LN::LPR) s_dw[wid][kd][lane * EPL + e] = x;
     }
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * D; c += kWarps * 32) {
+  for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
     float x = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) x += s_dw[w][c / D][c % D];
@@ -363,43 +435,39 @@ norm_rope_weights(NormRopeArgs a, int ctas) {
   }
 }
 
-// Heads per warp: a whole token while tokens alone give every SM sixteen
-// warps, fewer heads (down to one step of the warp) below that, where the
-// call is bound by latency.
-template <typename T, int D>
-int head_chunk(const NormRopeArgs& a) {
-  constexpr int RW = Lanes<T, D>::RW;
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int64_t tokens = (int64_t)a.B * a.n;
-  const int64_t want = (int64_t)sm_count() * 16;
-  int64_t chunk = (heads * tokens + want - 1) / want;
-  chunk = (chunk + RW - 1) / RW * RW;
-  return (int)(chunk < heads ? chunk : heads);
+// log2 of the tokens per tile: up to 16 while that leaves `want` tiles per
+// SM, fewer below, down to one, where the call is bound by latency.  The
+// forward pass asks for the four CTAs that an SM holds; the backward pass,
+// whose CTAs walk over several tiles, for 12, so that the last round is a
+// small part.
+int tile_log2(int64_t tokens, int per_sm) {
+  const int64_t want = (int64_t)sm_count() * per_sm;
+  int lt = 0;
+  while ((1 << (lt + 1)) <= kMaxTile && (tokens >> (lt + 1)) >= want) ++lt;
+  return lt;
 }
 
 template <typename T, int D>
-cudaError_t forward_as(NormRopeArgs a, cudaStream_t s) {
-  a.chunk = head_chunk<T, D>(a);
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int64_t units =
-      (int64_t)a.B * a.n * ((heads + a.chunk - 1) / a.chunk);
-  const int64_t ctas = (units + kWarps - 1) / kWarps;
+cudaError_t forward_as(const NormRopeArgs& a, cudaStream_t s) {
+  const int64_t tokens = (int64_t)a.B * a.n;
+  const int lt = tile_log2(tokens, 4);
+  const int64_t ctas = (tokens + (1 << lt) - 1) >> lt;
   if (ctas > 0x7FFFFFFF) return cudaErrorNotSupported;
-  return launch("norm_rope", norm_rope<T, D>, dim3((unsigned)ctas),
-                kWarps * 32, 0, s, a);
+  return launch("norm_rope", norm_rope<T, D>, dim3((unsigned)ctas), kThreads,
+                0, s, a, lt);
 }
 
 template <typename T, int D>
 cudaError_t backward_as(NormRopeArgs a, cudaStream_t s) {
-  a.chunk = head_chunk<T, D>(a);
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int64_t units =
-      (int64_t)a.B * a.n * ((heads + a.chunk - 1) / a.chunk);
-  int64_t ctas = (units + kWarps - 1) / kWarps;
+  const int64_t tokens = (int64_t)a.B * a.n;
+  const int lt = tile_log2(tokens, 12);
+  int64_t ctas = (tokens + (1 << lt) - 1) >> lt;
+  const int64_t most = (int64_t)sm_count() * 2;  // what is resident
+  if (ctas > most) ctas = most;
   if (ctas > kNormRopeMaxCtas) ctas = kNormRopeMaxCtas;
   if (!a.w[0] && !a.w[1]) a.partial = nullptr;
   const cudaError_t e = launch("norm_rope_backward", norm_rope_backward<T, D>,
-                               dim3((unsigned)ctas), kWarps * 32, 0, s, a);
+                               dim3((unsigned)ctas), kThreads, 0, s, a, lt);
   if (e != cudaSuccess || !a.partial) return e;
   return launch("norm_rope_weights", norm_rope_weights<D>, dim3(2 * D / 32),
                 1024, 0, s, a, (int)ctas);
