@@ -27,6 +27,9 @@ from .binding import _check, _dt, _ptr, _require
 _DTYPES = (torch.float32, torch.bfloat16)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _On:
     """`dev` current, and what is allocated inside belonging to `stream`; as
     a value, the raw stream to launch on."""
@@ -44,7 +47,7 @@ class _On:
             if torch.cuda.current_device() != dev.index:
                 self.guard = torch.cuda.device(dev)
             # torch.cuda.current_stream(dev).cuda_stream without the object
-            self.raw = torch._C._cuda_getCurrentRawStream(dev.index)
+            self.raw = _raw_stream(dev.index)
 
     def __enter__(self):
         if self.guard is not None:
@@ -79,12 +82,12 @@ _PARAMS = struct.Struct("PPifPiiPi4x")
 _NONE = (0, 0, 0, 0)
 
 
-def _token_major(t: Optional[torch.Tensor], name: str):
+def _token_major(t: Optional[torch.Tensor], name: str, B: int, n: int,
+                 H: int):
     """The ca_rows fields of a [B, n, H, d] tensor."""
     if t is None:
         return _NONE
     sb, st, sh, sd = t.stride()
-    B, n, H, _ = t.shape
     if sd != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     # the stride of a dimension of one element says nothing
@@ -92,12 +95,11 @@ def _token_major(t: Optional[torch.Tensor], name: str):
             sh if H > 1 else 0)
 
 
-def _head_major(t: Optional[torch.Tensor], name: str):
+def _head_major(t: Optional[torch.Tensor], name: str, B: int, n: int, H: int):
     """The ca_rows fields of a [B, H, n, d] tensor."""
     if t is None:
         return _NONE
     sb, sh, st, sd = t.stride()
-    B, H, n, _ = t.shape
     if sd != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     return (t.data_ptr(), sb if B > 1 else 0, st if n > 1 else 0,
@@ -180,17 +182,18 @@ def condensate_attn_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor],
                 if y is not None:
                     raise ValueError(f"{nm} given without its input")
             elif y is None:
-                y = torch.empty((B, H, n, d), dtype=x.dtype, device=dev)
+                y = x.new_empty((B, H, n, d))
             else:
                 _expect(y, nm, (B, H, n, d), q.dtype, dev)
             outs.append(y)
         code = binding.load().condensate_attn_norm_rope(
-            _ROWS3.pack(*_token_major(q, "q"), *_token_major(k, "k"),
-                        *_token_major(v, "v")),
+            _ROWS3.pack(*_token_major(q, "q", B, n, Hq),
+                        *_token_major(k, "k", B, n, Hkv),
+                        *_token_major(v, "v", B, n, Hkv)),
             _dt(q.dtype), B, n, Hq, Hkv, d, par,
-            _ROWS3.pack(*_head_major(outs[0], "Q"),
-                        *_head_major(outs[1], "K"),
-                        *_head_major(outs[2], "V")), s)
+            _ROWS3.pack(*_head_major(outs[0], "Q", B, n, Hq),
+                        *_head_major(outs[1], "K", B, n, Hkv),
+                        *_head_major(outs[2], "V", B, n, Hkv)), s)
     _check(code, "condensate_attn_norm_rope")
     return tuple(outs)
 
@@ -241,7 +244,7 @@ def condensate_attn_norm_rope_backward(
                 if x is not None:
                     raise ValueError(f"{nm} given without its gradient")
             elif x is None:
-                x = torch.empty((B, n, H, d), dtype=dt, device=dev)
+                x = g.new_empty((B, n, H, d))
             else:
                 _expect(x, nm, (B, n, H, d), dt, dev)
             outs.append(x)
@@ -257,14 +260,15 @@ def condensate_attn_norm_rope_backward(
         if workspace is not None:
             _require(workspace, "workspace")
         code = lib.condensate_attn_norm_rope_backward(
-            _ROWS3.pack(*_head_major(dQ, "dQ"), *_head_major(dK, "dK"),
-                        *_head_major(dV, "dV")),
-            _ROWS3.pack(*_token_major(q, "q"), *_token_major(k, "k"),
-                        *_NONE),
+            _ROWS3.pack(*_head_major(dQ, "dQ", B, n, Hq),
+                        *_head_major(dK, "dK", B, n, Hkv),
+                        *_head_major(dV, "dV", B, n, Hkv)),
+            _ROWS3.pack(*_token_major(q, "q", B, n, Hq),
+                        *_token_major(k, "k", B, n, Hkv), *_NONE),
             _dt(dt), B, n, Hq, Hkv, d, par,
-            _ROWS3.pack(*_token_major(outs[0], "dq"),
-                        *_token_major(outs[1], "dk"),
-                        *_token_major(outs[2], "dv")),
+            _ROWS3.pack(*_token_major(outs[0], "dq", B, n, Hq),
+                        *_token_major(outs[1], "dk", B, n, Hkv),
+                        *_token_major(outs[2], "dv", B, n, Hkv)),
             _ptr(dqw), _ptr(dkw), _ptr(workspace),
             0 if workspace is None else workspace.numel() *
             workspace.element_size(), s)
@@ -315,13 +319,16 @@ def condensate_attn_prefill_backward(
     with _On(dev, stream) as s:
         if dQ is None:
             dQ = torch.empty_like(Q)
+        else:
+            _dense(dQ, "dQ", Q.shape, dt, dev)
         if dK is None:
             dK = torch.empty_like(K)
+        else:
+            _dense(dK, "dK", K.shape, dt, dev)
         if dV is None:
             dV = torch.empty_like(V)
-        _dense(dQ, "dQ", Q.shape, dt, dev)
-        _dense(dK, "dK", K.shape, dt, dev)
-        _dense(dV, "dV", V.shape, dt, dev)
+        else:
+            _dense(dV, "dV", V.shape, dt, dev)
         if workspace is None:
             workspace = torch.empty(
                 condensate_attn_prefill_backward_workspace_size(
@@ -329,10 +336,10 @@ def condensate_attn_prefill_backward(
                 dtype=torch.uint8, device=dev)
         _require(workspace, "workspace")
         code = binding.load().condensate_attn_prefill_backward(
-            _ptr(Q), _ptr(K), _ptr(V), _dt(dt), _ptr(dO), _dt(dO.dtype), B,
-            nq, L, Hq, Hkv, d, int(W), int(k), _ptr(W_i), _ptr(W_h),
-            _ptr(idx), _ptr(idx_count), idx.shape[-1], _ptr(dQ), _ptr(dK),
-            _ptr(dV), _ptr(workspace),
+            Q.data_ptr(), K.data_ptr(), V.data_ptr(), _dt(dt), dO.data_ptr(),
+            _dt(dO.dtype), B, nq, L, Hq, Hkv, d, int(W), int(k), _ptr(W_i),
+            _ptr(W_h), idx.data_ptr(), idx_count.data_ptr(), idx.shape[-1],
+            dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), s)
     _check(code, "condensate_attn_prefill_backward")
     return dQ, dK, dV

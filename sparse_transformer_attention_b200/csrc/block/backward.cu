@@ -107,7 +107,7 @@ backward_split(const float4* x, uint2* hi, uint2* lo, int64_t n4) {
 }
 
 // ---------------------------------------------------------------- row pass
-// One warp per query row; eight lanes per key, four keys at a time.  One
+// One warp per query row; eight lanes per key, eight keys at a time.  One
 // sweep over the set with a running maximum m and, behind it, the sums
 //   l = sum e,  E = sum e dP,  A = sum e dP k,  Bk = sum e k   (e = 2^(x-m))
 // so that D = E / l and dQ = (A - D Bk) / l without a second reading.
@@ -176,43 +176,58 @@ __global__ void __launch_bounds__(kRowWarps * 32) backward_rows(Args a) {
 
   RowState<T, TD, D> st;
   st.clear();
-  // slots, then window keys, four at a time
+  // slots, then window keys, eight at a time (two per group)
   const int nw = i - lo + 1;
 #pragma unroll 1
-  for (int t0 = 0; t0 < ns + nw; t0 += 4) {
-    const int t = t0 + grp;
-    bool act = t < ns + nw;
-    int j = 0;
-    if (act) {
-      if (t >= ns) {
-        j = lo + t - ns;
-      } else if (t > 0) {
-        j = __ldg(ix + t);
-        if (j < 1 || j > i - w) {  // not a candidate of this row
-          if (sub == 0) raise_flag(a.status, kErrCmax);
-          act = false;
-          j = 0;
+  for (int t0 = 0; t0 < ns + nw; t0 += 8) {
+    constexpr int U = 2;
+    bool act[U];
+    int j[U];
+    float kf[U][DL], vf[U][DL];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + 4 * u + grp;
+      act[u] = t < ns + nw;
+      j[u] = 0;
+      if (act[u]) {
+        if (t >= ns) {
+          j[u] = lo + t - ns;
+        } else if (t > 0) {
+          j[u] = __ldg(ix + t);
+          if (j[u] < 1 || j[u] > i - w) {  // not a candidate of this row
+            if (sub == 0) raise_flag(a.status, kErrCmax);
+            act[u] = false;
+            j[u] = 0;
+          }
         }
+        if (t < ns && sub == 0)
+          key[t] = act[u] ? (uint32_t)j[u] : (uint32_t)a.L;
       }
-      if (t < ns && sub == 0) key[t] = act ? (uint32_t)j : (uint32_t)a.L;
-    }
-    float kf[DL], vf[DL];
-    load_row<T, DL>(K + (int64_t)j * D, kf);
-    load_row<T, DL>(V + (int64_t)j * D, vf);
-    float x = 0.f, dp = 0.f;
-#pragma unroll
-    for (int c = 0; c < DL; ++c) {
-      x = fmaf(q[c], kf[c], x);
-      dp = fmaf(g[c], vf[c], dp);
     }
 #pragma unroll
-    for (int off = 4; off > 0; off >>= 1) {
-      x += __shfl_xor_sync(kAll, x, off);
-      dp += __shfl_xor_sync(kAll, dp, off);
+    for (int u = 0; u < U; ++u) {
+      load_row<T, DL>(K + (int64_t)j[u] * D, kf[u]);
+      load_row<T, DL>(V + (int64_t)j[u] * D, vf[u]);
     }
-    x *= sl2;
-    if (t < ns && sub == 0) s_x[t] = make_float2(act ? x : -INFINITY, dp);
-    if (act) st.add(x, dp, kf);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + 4 * u + grp;
+      float x = 0.f, dp = 0.f;
+#pragma unroll
+      for (int c = 0; c < DL; ++c) {
+        x = fmaf(q[c], kf[u][c], x);
+        dp = fmaf(g[c], vf[u][c], dp);
+      }
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) {
+        x += __shfl_xor_sync(kAll, x, off);
+        dp += __shfl_xor_sync(kAll, dp, off);
+      }
+      x *= sl2;
+      if (t < ns && sub == 0)
+        s_x[t] = make_float2(act[u] ? x : -INFINITY, dp);
+      if (act[u]) st.add(x, dp, kf[u]);
+    }
   }
   // the four groups' states, merged
 #pragma unroll
@@ -380,7 +395,7 @@ backward_listed(Args a, const uint32_t* keys, const uint32_t* ents) {
 }
 
 // ------------------------------------------------------------- column pass
-// One warp per key: its window rows, eight lanes per row, four rows at a
+// One warp per key: its window rows, eight lanes per row, eight rows at a
 // time, then the listed part.
 template <typename T, typename TD, int D>
 __global__ void __launch_bounds__(256) backward_columns(Args a) {
@@ -406,31 +421,41 @@ __global__ void __launch_bounds__(256) backward_columns(Args a) {
     const int r0 = max(j - a.p0, 0);
     const int r1 = (int)min((int64_t)j + wm - 1 - a.p0, (int64_t)a.nq - 1);
     const int64_t rowbase = ((int64_t)b * a.Hq + h) * a.nq;
-    for (int rr = r0; rr <= r1; rr += 4) {
-      const int r = min(rr + grp, r1);
-      int w;
-      bool act = rr + grp <= r1 && window_lo(a, b, h, r, false, &w) <= j;
-      float qf[DL], of[DL];
-      load_row<T, DL>(reinterpret_cast<const T*>(a.Q) + (rowbase + r) * D + sub * DL, qf);
-      load_row<TD, DL>(reinterpret_cast<const TD*>(a.dO) + (rowbase + r) * D + sub * DL, of);
-      const float2 st = a.stats[rowbase + r];
-      float x = 0.f, dp = 0.f;
+    for (int rr = r0; rr <= r1; rr += 8) {
+      constexpr int U = 2;
+      bool act[U];
+      float qf[U][DL], of[U][DL];
+      float2 st[U];
 #pragma unroll
-      for (int c = 0; c < DL; ++c) {
-        x = fmaf(qf[c], kf[c], x);
-        dp = fmaf(of[c], vf[c], dp);
+      for (int u = 0; u < U; ++u) {
+        const int r = min(rr + 4 * u + grp, r1);
+        int w;
+        act[u] = rr + 4 * u + grp <= r1 &&
+                 window_lo(a, b, h, r, false, &w) <= j;
+        load_row<T, DL>(reinterpret_cast<const T*>(a.Q) + (rowbase + r) * D + sub * DL, qf[u]);
+        load_row<TD, DL>(reinterpret_cast<const TD*>(a.dO) + (rowbase + r) * D + sub * DL, of[u]);
+        st[u] = a.stats[rowbase + r];
       }
 #pragma unroll
-      for (int off = 4; off > 0; off >>= 1) {
-        x += __shfl_xor_sync(kAll, x, off);
-        dp += __shfl_xor_sync(kAll, dp, off);
-      }
-      const float p = act ? exp2f(x * sl2 - st.x) : 0.f;
-      const float ds = p * (dp - st.y) * sc;
+      for (int u = 0; u < U; ++u) {
+        float x = 0.f, dp = 0.f;
 #pragma unroll
-      for (int c = 0; c < DL; ++c) {
-        dk[c] = fmaf(ds, qf[c], dk[c]);
-        dv[c] = fmaf(p, of[c], dv[c]);
+        for (int c = 0; c < DL; ++c) {
+          x = fmaf(qf[u][c], kf[c], x);
+          dp = fmaf(of[u][c], vf[c], dp);
+        }
+#pragma unroll
+        for (int off = 4; off > 0; off >>= 1) {
+          x += __shfl_xor_sync(kAll, x, off);
+          dp += __shfl_xor_sync(kAll, dp, off);
+        }
+        const float p = act[u] ? exp2f(x * sl2 - st[u].x) : 0.f;
+        const float ds = p * (dp - st[u].y) * sc;
+#pragma unroll
+        for (int c = 0; c < DL; ++c) {
+          dk[c] = fmaf(ds, qf[u][c], dk[c]);
+          dv[c] = fmaf(p, of[u][c], dv[c]);
+        }
       }
     }
   }

@@ -22,8 +22,13 @@ constexpr int kSteps = kTile / kThreads;  // entries per thread
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallSteps = 16;
 constexpr int kSmall = kSmallThreads * kSmallSteps;
+constexpr int kSmallDigit = 9;  // bits of a digit at most
+// two buffers of keys and 16-bit entry numbers, each warp's digit counts
 constexpr size_t kSmallSmem =
-    (size_t)kSmall * 8 + (size_t)(kSmallThreads / 32) * 256 * 2;
+    (size_t)kSmall * 12 +
+    (size_t)(kSmallThreads / 32) * (1 << kSmallDigit) * 2;
+static_assert(kSmall <= 65536, "places and entries fit 16 bits");
+static_assert(kSmallSmem <= 232448 - 1024, "fits an SM");
 
 __global__ void __launch_bounds__(kThreads)
 sort_count(Args a, const uint32_t* key, int shift, uint32_t mask) {
@@ -77,15 +82,16 @@ __global__ void __launch_bounds__(256) sort_scan(Args a) {
   if (lane == 0) a.totals[at] = sum;
 }
 
-// Exclusive scan over the CTA's first 256 threads (the others pass 0).
+// Exclusive scan over the CTA's first 32 * W threads (the others pass 0).
+template <int W>
 __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t* s_warp) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const uint32_t x = warp_scan(v, lane);
-  if (lane == 31 && wid < 8) s_warp[wid] = x;
+  if (lane == 31 && wid < W) s_warp[wid] = x;
   __syncthreads();
   uint32_t before = 0;
 #pragma unroll
-  for (int w = 0; w < 8; ++w)
+  for (int w = 0; w < W; ++w)
     if (w < wid) before += s_warp[w];
   __syncthreads();
   return before + x - v;
@@ -96,7 +102,7 @@ __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t* s_warp) {
 __device__ __forceinline__ uint32_t peers(uint32_t dg, int bits) {
   uint32_t same = kAll;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < kSmallDigit; ++i) {
     if (i < bits) {
       const uint32_t set = __ballot_sync(kAll, (dg >> i) & 1u);
       same &= ((dg >> i) & 1u) ? set : ~set;
@@ -105,28 +111,20 @@ __device__ __forceinline__ uint32_t peers(uint32_t dg, int bits) {
   return same;
 }
 
-// Ranks a warp's run of STEPS x 32 entries in order: equal digits of a step
-// by lane, earlier steps by the running counts cnt[256].  Entries behind the
-// end (live 0) are a tail of the run.
-template <int STEPS>
-__device__ __forceinline__ void rank_run(const uint32_t (&kv)[STEPS],
-                                         uint32_t (&rank)[STEPS], int live,
-                                         int shift, uint32_t mask, int bits,
-                                         uint16_t* cnt) {
+// The rank of this lane's entry among a warp's entries of its digit: equal
+// digits of the step by lane, earlier steps by the running counts cnt.
+// Entries behind the end (!in) are the last lanes.
+__device__ __forceinline__ uint32_t rank_step(uint32_t dg, bool in, int bits,
+                                              uint16_t* cnt) {
   const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int u = 0; u < STEPS; ++u) {
-    const bool in = u * 32 + lane < live;
-    const uint32_t dg = (kv[u] >> shift) & mask;
-    const uint32_t same = peers(dg, bits) & __ballot_sync(kAll, in);
-    const uint32_t lower = same & ((1u << lane) - 1u);
-    uint32_t before = 0;
-    if (in) before = cnt[dg];
-    __syncwarp();
-    if (in && lower == 0) cnt[dg] = (uint16_t)(before + __popc(same));
-    __syncwarp();
-    rank[u] = before + __popc(lower);
-  }
+  const uint32_t same = peers(dg, bits) & __ballot_sync(kAll, in);
+  const uint32_t lower = same & ((1u << lane) - 1u);
+  uint32_t before = 0;
+  if (in) before = cnt[dg];
+  __syncwarp();
+  if (in && lower == 0) cnt[dg] = (uint16_t)(before + __popc(same));
+  __syncwarp();
+  return before + __popc(lower);
 }
 
 // Places a tile: the warps' runs are ranked, their counts chained, and the
@@ -160,15 +158,18 @@ sort_place(Args a, const uint32_t* key, const uint32_t* ent, uint32_t* key_out,
   for (int c = threadIdx.x; c < kWarps * 256; c += kThreads)
     (&cnt[0][0])[c] = 0;
   __syncthreads();
-  rank_run<kSteps>(kv, rank, n - l0, shift, mask, a.w.digit, cnt[wid]);
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u)
+    rank[u] = rank_step((kv[u] >> shift) & mask, l0 + u * 32 + lane < n,
+                        a.w.digit, cnt[wid]);
   __syncthreads();
   {
     uint32_t total = 0;
     if (mine)
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) total += cnt[w][dg];
-    const uint32_t local = cta_scan(total, s_warp);
-    const uint32_t first = cta_scan(all, s_warp);
+    const uint32_t local = cta_scan<8>(total, s_warp);
+    const uint32_t first = cta_scan<8>(all, s_warp);
     if (mine) {
       s_dst[dg] = first + prior - local;
       uint32_t x = local;
@@ -208,75 +209,82 @@ sort_place(Args a, const uint32_t* key, const uint32_t* ent, uint32_t* key_out,
 
 // All passes over one kv head's list, one CTA, the list in shared memory.
 __global__ void __launch_bounds__(kSmallThreads)
-sort_small(Args a, const uint32_t* key, uint32_t* key_out, uint32_t* ent_out) {
-  constexpr int kW = kSmallThreads / 32;
+sort_small(Args a, const uint32_t* key, uint32_t* key_out, uint32_t* ent_out,
+           int passes, int digit) {
+  constexpr int kW = kSmallThreads / 32, kDigits = 1 << kSmallDigit;
   extern __shared__ __align__(16) unsigned char g_smem[];
-  __shared__ uint32_t s_warp[8];
+  __shared__ uint32_t s_warp[kDigits / 32];
   chain();
-  uint32_t* s_key = reinterpret_cast<uint32_t*>(g_smem);
-  uint32_t* s_ent = s_key + kSmall;
-  uint16_t(*cnt)[256] = reinterpret_cast<uint16_t(*)[256]>(s_ent + kSmall);
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(g_smem);  // [2][kSmall]
+  uint16_t* s_ent = reinterpret_cast<uint16_t*>(s_key + 2 * kSmall);
+  uint16_t(*cnt)[kDigits] =
+      reinterpret_cast<uint16_t(*)[kDigits]>(s_ent + 2 * kSmall);
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int64_t base = (int64_t)blockIdx.x * a.w.per_head;
   const int n = (int)a.w.per_head;
   // a warp's run: as many steps as the list needs
   const int steps = (n + kSmallThreads - 1) / kSmallThreads;
   const int l0 = wid * 32 * steps;
-  const uint32_t mask = (1u << a.w.digit) - 1u;
-  uint32_t kv[kSmallSteps], ev[kSmallSteps], rank[kSmallSteps];
-#pragma unroll
-  for (int u = 0; u < kSmallSteps; ++u) {
-    const int l = l0 + u * 32 + lane;
-    kv[u] = u < steps && l < n ? key[base + l] : 0u;
-    ev[u] = (uint32_t)l;
+  const uint32_t mask = (1u << digit) - 1u;
+  for (int l = threadIdx.x; l < n; l += kSmallThreads) {
+    s_key[l] = key[base + l];
+    s_ent[l] = (uint16_t)l;
   }
-  for (int p = 0; p < a.w.passes; ++p) {
-    const int shift = p * a.w.digit;
-    for (int c = threadIdx.x; c < kW * 256; c += kSmallThreads)
-      (&cnt[0][0])[c] = 0;
+  for (int p = 0; p < passes; ++p) {
+    const int shift = p * digit;
+    const uint32_t* from = s_key + (p & 1) * kSmall;
+    const uint16_t* efrom = s_ent + (p & 1) * kSmall;
+    uint32_t* to = s_key + (p & 1 ^ 1) * kSmall;
+    uint16_t* eto = s_ent + (p & 1 ^ 1) * kSmall;
+    for (int c = threadIdx.x; c < kW * kDigits / 2; c += kSmallThreads)
+      reinterpret_cast<uint32_t*>(&cnt[0][0])[c] = 0;
     __syncthreads();
+    uint16_t rank[kSmallSteps];
 #pragma unroll
-    for (int u = 0; u < kSmallSteps; ++u)
-      if (u < steps) {
-        uint32_t k1[1] = {kv[u]}, r1[1];
-        rank_run<1>(k1, r1, n - l0 - u * 32, shift, mask, a.w.digit, cnt[wid]);
-        rank[u] = r1[0];
-      }
+    for (int u = 0; u < kSmallSteps; ++u) {
+      if (u >= steps) break;
+      const int l = l0 + u * 32 + lane;
+      rank[u] = (uint16_t)rank_step(l < n ? (from[l] >> shift) & mask : 0u,
+                                    l < n, digit, cnt[wid]);
+    }
     __syncthreads();
+    // a digit's entries in each warp's run, chained over the warps
     const int dg = threadIdx.x;
-    uint32_t total = 0;
-    if (dg < 256)
-      for (int w = 0; w < kW; ++w) total += cnt[w][dg];
-    uint32_t x = cta_scan(total, s_warp);
-    if (dg < 256)
-      for (int w = 0; w < kW; ++w) {
-        const uint32_t c = cnt[w][dg];
-        cnt[w][dg] = (uint16_t)x;
-        x += c;
-      }
-    __syncthreads();
+    uint32_t c[kW], total = 0;
+    if (dg < kDigits) {
 #pragma unroll
-    for (int u = 0; u < kSmallSteps; ++u)
-      if (u < steps && l0 + u * 32 + lane < n) {
-        const uint32_t at = cnt[wid][(kv[u] >> shift) & mask] + rank[u];
-        if (in_bounds(at < (uint32_t)kSmall, a.status)) {
-          s_key[at] = kv[u];
-          s_ent[at] = ev[u];
-        }
+      for (int w = 0; w < kW; ++w) c[w] = cnt[w][dg];
+#pragma unroll
+      for (int w = 0; w < kW; ++w) total += c[w];
+    }
+    uint32_t x = cta_scan<kDigits / 32>(total, s_warp);
+    if (dg < kDigits) {
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        cnt[w][dg] = (uint16_t)x;
+        x += c[w];
       }
+    }
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kSmallSteps; ++u) {
+      if (u >= steps) break;
       const int l = l0 + u * 32 + lane;
-      if (u < steps && l < n) {
-        kv[u] = s_key[l];
-        ev[u] = s_ent[l];
+      if (l < n) {
+        const uint32_t kv = from[l];
+        const uint32_t at = cnt[wid][(kv >> shift) & mask] + (uint32_t)rank[u];
+        if (in_bounds(at < (uint32_t)kSmall, a.status)) {
+          to[at] = kv;
+          eto[at] = efrom[l];
+        }
       }
     }
+    __syncthreads();
   }
+  const int last = passes & 1;
   for (int l = threadIdx.x; l < n; l += kSmallThreads) {
-    key_out[base + l] = s_key[l];
-    ent_out[base + l] = s_ent[l];
+    key_out[base + l] = s_key[last * kSmall + l];
+    ent_out[base + l] = s_ent[last * kSmall + l];
   }
 }
 
@@ -285,12 +293,13 @@ sort_small(Args a, const uint32_t* key, uint32_t* key_out, uint32_t* ent_out) {
 cudaError_t sort_launch(const Args& a, int* last, cudaStream_t s) {
   const Work& w = a.w;
   if (w.per_head <= kSmall) {
-    static_assert(kSmall <= 65536, "places fit 16 bits");
     const cudaError_t e = ensure_smem(sort_small, kSmallSmem);
     if (e != cudaSuccess) return e;
     *last = 1;
+    const int passes = (w.bits + kSmallDigit - 1) / kSmallDigit;
     return launch("sort_small", sort_small, dim3(w.segs), kSmallThreads,
-                  kSmallSmem, s, a, a.key[0], a.key[1], a.ent[1]);
+                  kSmallSmem, s, a, a.key[0], a.key[1], a.ent[1], passes,
+                  (w.bits + passes - 1) / passes);
   }
   const dim3 grid(w.tiles, w.segs);
   int from = 0;
