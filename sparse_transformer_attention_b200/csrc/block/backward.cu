@@ -25,8 +25,8 @@ using namespace bwd;
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-bool plan(Work& w, bool planes, int B, int nq, int L, int Hq, int Hkv, int d,
-          int k) {
+bool plan(Work& w, bool bf16, bool do_bf16, int B, int nq, int L, int Hq,
+          int Hkv, int d, int k) {
   w.rows = (int64_t)B * Hq * nq;
   w.segs = B * Hkv;
   const int64_t per = (int64_t)(Hq / Hkv) * nq * (k + 1);
@@ -60,7 +60,8 @@ bool plan(Work& w, bool planes, int B, int nq, int L, int Hq, int Hkv, int d,
   w.totals = take((size_t)w.segs * 256 * 4);
   w.top = take((size_t)w.segs * L * 2 * d * 4);
   w.carry = take((size_t)w.segs * w.ranges * 2 * d * 4);
-  w.planes = take(planes ? (size_t)w.rows * d * 4 : 0);
+  w.planes = take(bf16 && !do_bf16 ? (size_t)w.rows * d * 4 : 0);
+  w.dql = take(bf16 ? (size_t)w.rows * d * 4 : 0);
   w.total = at;
   return true;
 }
@@ -541,14 +542,14 @@ cudaError_t launch_as(Args a, cudaStream_t s) {
 size_t backward_workspace(bool bf16, bool do_bf16, int B, int nq, int L,
                           int Hq, int Hkv, int d, int k) {
   Work w;
-  return plan(w, bf16 && !do_bf16, B, nq, L, Hq, Hkv, d, k) ? w.total : 0;
+  return plan(w, bf16, do_bf16, B, nq, L, Hq, Hkv, d, k) ? w.total : 0;
 }
 
 cudaError_t backward_launch(const BackwardArgs& in, bool bf16, int d, void* ws,
                             cudaStream_t s) {
   Args a;
   static_cast<BackwardArgs&>(a) = in;
-  if (!plan(a.w, bf16 && !a.do_bf16, a.B, a.nq, a.L, a.Hq, a.Hkv, d, a.k))
+  if (!plan(a.w, bf16, a.do_bf16, a.B, a.nq, a.L, a.Hq, a.Hkv, d, a.k))
     return cudaErrorNotSupported;
   char* p = (char*)ws;
   a.wmax = (int*)(p + a.w.wmax);
@@ -566,6 +567,7 @@ cudaError_t backward_launch(const BackwardArgs& in, bool bf16, int d, void* ws,
   a.carry = (float*)(p + a.w.carry);
   a.g[0] = (const __nv_bfloat16*)(p + a.w.planes);
   a.g[1] = a.g[0] + a.w.rows * d;
+  a.dql = (float*)(p + a.w.dql);
   // the status area and, behind it, the window maxima and the keys' spans
   cudaError_t e = cudaMemsetAsync(ws, 0, a.w.lows, s);
   if (e != cudaSuccess) return e;

@@ -26,7 +26,7 @@ struct Work {
   int ranges;        // listed-pass ranges per segment
   int bits, passes, digit;  // key bits; sort passes; bits of each
   size_t wmax, lows, stats, pds, key[2], ent[2], hist, totals, span, top,
-      carry, planes, total;
+      carry, planes, dql, total;
 };
 
 struct Args : BackwardArgs {
@@ -46,6 +46,7 @@ struct Args : BackwardArgs {
   // dO in bf16: dO itself, or an fp32 dO as two planes, dO = hi + lo up to
   // 2^-16 of its value
   const __nv_bfloat16* g[2];
+  float* dql;  // bf16: [B, Hq, nq, d] listed part of dQ
 };
 
 // The window of query row r of head h: [lo, i].

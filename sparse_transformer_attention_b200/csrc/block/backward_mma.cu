@@ -108,18 +108,20 @@ constexpr int kWarpRows = 64 / kRowWarps;  // Top-k rows of a warp
 
 template <int D, int NP>
 struct RowSmem {
-  static constexpr int CK = 64;         // keys of a chunk
+  static constexpr int CK = D == 64 ? 64 : 32;  // keys of a chunk
   static constexpr int RS = D * 2 + 16; // padded row (bytes)
   static constexpr size_t rows = (size_t)(NP + 1) * 64 * RS;   // q, dO
   static constexpr size_t chunk = (size_t)2 * CK * RS;         // K, V
   static constexpr size_t anchor = (size_t)2 * 16 * RS;        // K, V
-  static constexpr int DS = D + 8;  // dQ row: no two of 8 rows on a bank
-  static constexpr size_t dq = (size_t)64 * DS * 4;
+  // dQ's window part, in the chunks' place at the end: rows of DS floats, no
+  // two of 8 rows on a bank
+  static constexpr int DS = D + 8;
+  static_assert((size_t)64 * DS * 4 <= 2 * chunk, "dQ fits the chunks");
   static constexpr size_t stat = (size_t)64 * 4;  // one number per row
   __host__ __device__ static size_t bytes(int k) {
     const size_t kk = (k + 15) / 16 * 16;
     // 2 x 3 running sums, the log-sum-exp, D, the Top-k count
-    return rows + 2 * chunk + anchor + dq + 9 * stat +
+    return rows + 2 * chunk + anchor + 9 * stat +
            kRowWarps * kk * 8 + 64 * kk * 4;
   }
 };
@@ -200,12 +202,15 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 template <int D, int NP>
-__global__ void __launch_bounds__(kRowWarps * 32, D == 64 ? 2 : 1)
+__global__ void __launch_bounds__(kRowWarps * 32, 2)
 backward_rows_mma(Args a, int ntile) {
   using SM = RowSmem<D, NP>;
   constexpr int RS = SM::RS, CK = SM::CK, DS = SM::DS;
   constexpr int KS = D / 16;  // steps of a product over the head dimension
   constexpr int NT = D / 8;   // its 8-wide tiles
+  // q's and dO's operands of the window products: in registers where they
+  // leave room for two CTAs per SM, else read with every block
+  constexpr bool kHold = D == 64 && NP == 1;
   extern __shared__ __align__(16) unsigned char g_smem[];
   chain();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -224,8 +229,8 @@ backward_rows_mma(Args a, int ntile) {
   unsigned char* sR = g_smem;              // q and dO
   unsigned char* sC = sR + SM::rows;       // two chunks of K and V
   unsigned char* sA = sC + 2 * SM::chunk;  // the first 16 keys
-  float* s_dq = reinterpret_cast<float*>(sA + SM::anchor);
-  float* s_part = s_dq + 64 * DS;  // [half][m, l, E][row]
+  float* s_part = reinterpret_cast<float*>(sA + SM::anchor);  // [half][m, l,
+                                                              //  E][row]
   float* s_lse = s_part + 6 * 64;
   float* s_D = s_lse + 64;
   int* s_top = reinterpret_cast<int*>(s_D + 64);  // Top-k entries of a row
@@ -337,47 +342,52 @@ backward_rows_mma(Args a, int ntile) {
       __any_sync(kAll, (va && loa > 0) || (vb && lob > 0)) && hf == 0 && wlive;
   asm volatile("cp.async.wait_group 1;" ::: "memory");
   __syncthreads();
-  // A operands of the window products: q and dO of the warp's rows
-  uint32_t qa[KS][4], ga[NP][KS][4];
-  auto fragments = [&]() {
-    const unsigned char* at =
-        sR + (rg * 16 + (lane & 15)) * RS + (lane >> 4) * 16;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      ldsm4(qa[ks], at + ks * 32);
-#pragma unroll
-      for (int p = 0; p < NP; ++p)
-        ldsm4(ga[p][ks], at + (size_t)(p + 1) * 64 * RS + ks * 32);
-    }
+  // A operands of the window products: q (plane 0) and dO of the warp's rows
+  auto operand = [&](int plane, int ks, uint32_t (&A)[4]) {
+    ldsm4(A, sR + (size_t)plane * 64 * RS +
+                 (rg * 16 + (lane & 15)) * RS + (lane >> 4) * 16 + ks * 32);
   };
-  fragments();
+  uint32_t held[kHold ? 2 : 1][kHold ? KS : 1][4];
+  auto hold = [&]() {
+    if constexpr (kHold)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) operand(p, ks, held[p][ks]);
+  };
+  hold();
   // scores (log2 units, masked to -inf) and dP of the 16 x 16 block of keys
   // kb.. (at place kl of the staged chunk), as two accumulators of 8 keys
   auto block = [&](const unsigned char* sk, int stride, int kb, bool anchor,
                    float (&x)[2][4], float (&dp)[2][4]) {
     const unsigned char* at = sk + ((lane & 7) + ((lane >> 4) << 3)) * RS +
                               ((lane >> 3) & 1) * 16;
-    auto step = [&](float (&d)[4], const uint32_t (&A)[4], uint32_t b0,
-                    uint32_t b1, bool first) {
-      if (first) mma0(d, A[0], A[1], A[2], A[3], b0, b1);
-      else mma(d, A[0], A[1], A[2], A[3], b0, b1);
+    auto step = [&](float (&d)[2][4], int plane, int ks,
+                    const uint32_t (&f)[4], bool first) {
+      uint32_t A[4];
+      if constexpr (kHold) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) A[c] = held[plane][ks][c];
+      } else {
+        operand(plane, ks, A);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (first) mma0(d[t], A[0], A[1], A[2], A[3], f[2 * t], f[2 * t + 1]);
+        else mma(d[t], A[0], A[1], A[2], A[3], f[2 * t], f[2 * t + 1]);
     };
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       uint32_t f[4];
       ldsm4(f, at + ks * 32);
-      step(x[0], qa[ks], f[0], f[1], ks == 0);
-      step(x[1], qa[ks], f[2], f[3], ks == 0);
+      step(x, 0, ks, f, ks == 0);
     }
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       uint32_t f[4];
       ldsm4(f, at + stride * RS + ks * 32);
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        step(dp[0], ga[p][ks], f[0], f[1], ks == 0 && p == 0);
-        step(dp[1], ga[p][ks], f[2], f[3], ks == 0 && p == 0);
-      }
+      for (int p = 0; p < NP; ++p) step(dp, p + 1, ks, f, ks == 0 && p == 0);
     }
     if (!anchor && kb >= inner_lo && kb + 15 <= inner_hi) {  // seen by all
 #pragma unroll
@@ -604,17 +614,25 @@ backward_rows_mma(Args a, int ntile) {
         a.stats[row] = make_float2(lse, Di);
       }
       // lanes tq = 0 (2) hold A of the lines' first (second) halves, tq = 1
-      // (3) Bk: dimensions 8 (gr / 2) + gr % 2 + {0, 2, 4, 6} of a half
+      // (3) Bk: dimensions 8 (gr / 2) + gr % 2 + {0, 2, 4, 6} of a half.  dQ's
+      // listed part goes out as four consecutive values per lane.
 #pragma unroll
-      for (int t = 0; t < 2 * NL; ++t)
+      for (int c = 0; c < NL; ++c) {
+        float v[4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float v = acc[t][2 * u] + acc[t][2 * u + 1];
-          const float o = __shfl_down_sync(kAll, v, 1);
-          if ((tq & 1) == 0)
-            s_dq[tr * DS + 64 * (t >> 1) + 16 * tq + 8 * kq + half +
-                 4 * (t & 1) + 2 * u] = (v - Di * o) * inv * sc;
+        for (int u = 0; u < 4; ++u) {
+          const float* t = acc[2 * c + (u >> 1)] + 2 * (u & 1);
+          const float x = t[0] + t[1];
+          v[u] = (x - Di * __shfl_down_sync(kAll, x, 1)) * inv * sc;
         }
+        const float o0 = __shfl_xor_sync(kAll, half ? v[0] : v[2], 4);
+        const float o1 = __shfl_xor_sync(kAll, half ? v[1] : v[3], 4);
+        if ((tq & 1) == 0)
+          *reinterpret_cast<float4*>(a.dql + row * D + 64 * c + 16 * tq +
+                                     8 * kq + 4 * half) =
+              half ? make_float4(o0, v[2], o1, v[3])
+                   : make_float4(v[0], o0, v[1], o1);
+      }
       __syncwarp();
       float2* pds = a.pds + row * (k + 1);
       for (int t = lane; t < k; t += 32) {
@@ -632,13 +650,25 @@ backward_rows_mma(Args a, int ntile) {
 
   // ---- 3: dS of the window and the anchor
   __syncthreads();
-  float o[NT][4];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[t][c] = 0.f;
+  float o[NT][4];  // of the pair's first warp with the listed part
   {
-    fragments();
+    const float* pa = a.dql + (rowbase + ca) * D + 2 * tq;
+    const float* pb = a.dql + (rowbase + cb) * D + 2 * tq;
+    const float2 zero = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float2 x = hf == 0 && va
+          ? __ldcg(reinterpret_cast<const float2*>(pa + 8 * t)) : zero;
+      const float2 y = hf == 0 && vb
+          ? __ldcg(reinterpret_cast<const float2*>(pb + 8 * t)) : zero;
+      o[t][0] = x.x;
+      o[t][1] = x.y;
+      o[t][2] = y.x;
+      o[t][3] = y.y;
+    }
+  }
+  {
+    hold();
     const int sr = rg * 16 + gr;
     const float lse[2] = {s_lse[sr], s_lse[sr + 8]};
     const float Di[2] = {s_D[sr], s_D[sr + 8]};
@@ -688,7 +718,9 @@ backward_rows_mma(Args a, int ntile) {
         add(sC + (ch & 1) * SM::chunk + (kb - cs) * RS, CK, kb, false);
     }
   }
-  // dQ: the listed part, then the two warps' window parts, in this order
+  // dQ: the pair's first warp's part, then the second's
+  __syncthreads();
+  float* s_dq = reinterpret_cast<float*>(sC);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     if (u == hf) {
@@ -697,7 +729,11 @@ backward_rows_mma(Args a, int ntile) {
         float2* pa = reinterpret_cast<float2*>(
             s_dq + (rg * 16 + gr) * DS + 8 * t + 2 * tq);
         float2* pb = pa + 4 * DS;
-        const float2 x = *pa, y = *pb;
+        float2 x = make_float2(0.f, 0.f), y = x;
+        if (u == 1) {
+          x = *pa;
+          y = *pb;
+        }
         *pa = make_float2(x.x + o[t][0], x.y + o[t][1]);
         *pb = make_float2(y.x + o[t][2], y.y + o[t][3]);
       }
