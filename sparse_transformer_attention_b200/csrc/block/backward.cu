@@ -25,6 +25,12 @@ using namespace bwd;
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Warps per CTA of the listed pass, and the ranges they sum side by side.
+constexpr int kListedWarps = 4;
+constexpr int listed_ranges(bool bf16, int d) {
+  return kListedWarps * 32 * (bf16 ? 8 : 4) / d;
+}
+
 bool plan(Work& w, bool bf16, bool do_bf16, int B, int nq, int L, int Hq,
           int Hkv, int d, int k) {
   w.rows = (int64_t)B * Hq * nq;
@@ -36,6 +42,8 @@ bool plan(Work& w, bool bf16, bool do_bf16, int B, int nq, int L, int Hq,
   w.per_head = per;
   w.tiles = (int)((per + kTile - 1) / kTile);
   w.ranges = (int)((per + kRange - 1) / kRange);
+  w.per_block = listed_ranges(bf16, d);
+  w.blocks = w.ranges / w.per_block;
   w.bits = 1;
   while (((int64_t)1 << w.bits) <= L) ++w.bits;  // keys 0..L
   w.passes = (w.bits + 7) / 8;
@@ -60,6 +68,7 @@ bool plan(Work& w, bool bf16, bool do_bf16, int B, int nq, int L, int Hq,
   w.totals = take((size_t)w.segs * 256 * 4);
   w.top = take((size_t)w.segs * L * 2 * d * 4);
   w.carry = take((size_t)w.segs * w.ranges * 2 * d * 4);
+  w.bsum = take((size_t)w.segs * w.blocks * 2 * d * 4);
   w.planes = take(bf16 && !do_bf16 ? (size_t)w.rows * d * 4 : 0);
   w.dql = take(bf16 ? (size_t)w.rows * d * 4 : 0);
   w.total = at;
@@ -273,7 +282,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) backward_rows(Args a) {
 // row, 16 bytes each (8 to 32 lanes; a warp works on one to four ranges side
 // by side), key after key, so that the work is even however many rows list a
 // key.  A key's sum goes to `top` if it began in this range, else (the
-// range's head) to `carry`.
+// range's head) to `carry`; a CTA whose ranges all continue one key (the
+// anchor's list is as long as the rows) adds them up, too.
 //
 // Bound by what reaches a row's registers: 256 bytes of q and dO per entry
 // (bf16, d = 64), read anywhere in the head's rows.  With eight neighbouring
@@ -281,8 +291,6 @@ __global__ void __launch_bounds__(kRowWarps * 32) backward_rows(Args a) {
 // matrix-instruction layouts, which need rows spread over lanes in steps of
 // four, take 8 to 16 and left that pipe full (92% of its cycles) at 290 us in
 // the 8K GPT-2-small case.  Plain fp32 FMA keep the weights whole, too.
-constexpr int kListedWarps = 4;
-
 template <typename T, typename TD, int D>
 __global__ void __launch_bounds__(kListedWarps * 32)
 backward_listed(Args a, const uint32_t* keys, const uint32_t* ents) {
@@ -296,10 +304,18 @@ backward_listed(Args a, const uint32_t* keys, const uint32_t* ents) {
   const int sub = lane / LPR, sl = lane % LPR;
   const int seg = blockIdx.y;
   const int64_t first = ((int64_t)blockIdx.x * kListedWarps + wid) * SUBS;
-  if (first >= a.w.ranges) return;  // no barrier of the CTA in this kernel
+  if (first >= a.w.ranges) return;  // not in a whole block: no barrier there
   const int64_t base = (int64_t)seg * a.w.per_head;
   const int64_t w0 = first * kRange;  // the warp's first entry
   const uint32_t L = (uint32_t)a.L;
+  // does the whole CTA continue one key?
+  constexpr int kBlock = kListedWarps * SUBS * kRange;
+  const int64_t b0 = (int64_t)blockIdx.x * kBlock;
+  bool whole = false;
+  if (b0 > 0 && b0 + kBlock <= a.w.per_head) {
+    const uint32_t k0 = keys[base + b0 - 1], k1 = keys[base + b0 + kBlock - 1];
+    whole = k0 == k1 && k1 < L;
+  }
   // the warp's entries: key, row, p, dS; where keys begin and end
   uint4* ent = s_ent[wid];
   {
@@ -393,6 +409,24 @@ backward_listed(Args a, const uint32_t* keys, const uint32_t* ents) {
     }
   }
   flush();
+  if (!whole) return;
+  __syncthreads();  // the entries have been read
+  float* sums = reinterpret_cast<float*>(&s_ent[0][0]);  // [range][2 D]
+  {
+    float* o = sums + (wid * SUBS + sub) * 2 * D + sl * EPL;
+#pragma unroll
+    for (int c = 0; c < EPL; ++c) {
+      o[c] = dk[c];
+      o[D + c] = dv[c];
+    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * D; c += kListedWarps * 32) {
+    float x = 0.f;
+#pragma unroll
+    for (int r = 0; r < kListedWarps * SUBS; ++r) x += sums[r * 2 * D + c];
+    a.bsum[((int64_t)seg * a.w.blocks + blockIdx.x) * 2 * D + c] = x;
+  }
 }
 
 // ------------------------------------------------------------- column pass
@@ -523,7 +557,7 @@ cudaError_t launch_as(Args a, cudaStream_t s) {
   int last;
   if ((e = sort_launch(a, &last, s)) != cudaSuccess) return e;
   const uint32_t *keys = a.key[last], *ents = a.ent[last];
-  constexpr int kPer = kListedWarps * 32 * Elem<T>::kPer16B / D;  // ranges
+  constexpr int kPer = listed_ranges(kMma, D);
   e = launch("backward_listed", backward_listed<T, TD, D>,
           dim3((w.ranges + kPer - 1) / kPer, w.segs), kListedWarps * 32, 0, s,
           a, keys, ents);
@@ -565,6 +599,7 @@ cudaError_t backward_launch(const BackwardArgs& in, bool bf16, int d, void* ws,
   a.span = (int2*)(p + a.w.span);
   a.top = (float*)(p + a.w.top);
   a.carry = (float*)(p + a.w.carry);
+  a.bsum = (float*)(p + a.w.bsum);
   a.g[0] = (const __nv_bfloat16*)(p + a.w.planes);
   a.g[1] = a.g[0] + a.w.rows * d;
   a.dql = (float*)(p + a.w.dql);

@@ -16,7 +16,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // in the order of idx; unused slots hold key L, which sorts behind all keys.
 constexpr int kTile = 4096;   // entries per CTA of the sort
 constexpr int kRange = 64;    // sorted entries of a sum of the listed pass
-constexpr int kRowChunk = 32; // query rows staged at a time by the columns
+constexpr int kRowChunk = 32; // query rows with one lowest window start
 
 struct Work {
   int64_t rows;      // B * Hq * nq
@@ -24,9 +24,11 @@ struct Work {
   int segs;          // B * Hkv
   int tiles;         // sort tiles per segment
   int ranges;        // listed-pass ranges per segment
+  int per_block;     // ranges summed by one CTA of the listed pass
+  int blocks;        // whole ones of those per segment
   int bits, passes, digit;  // key bits; sort passes; bits of each
   size_t wmax, lows, stats, pds, key[2], ent[2], hist, totals, span, top,
-      carry, planes, dql, total;
+      carry, bsum, planes, dql, total;
 };
 
 struct Args : BackwardArgs {
@@ -43,6 +45,8 @@ struct Args : BackwardArgs {
   float* top;      // [segs, L, 2, d] listed part of dK and dV
   float* carry;    // [segs, ranges, 2, d] a range's share of the key that
                    // began in an earlier range
+  float* bsum;     // [segs, blocks, 2, d] sum of a block's shares, where the
+                   // whole block continues one key
   // dO in bf16: dO itself, or an fp32 dO as two planes, dO = hi + lo up to
   // 2^-16 of its value
   const __nv_bfloat16* g[2];

@@ -300,17 +300,18 @@ backward_rows_mma(Args a, int ntile) {
     for (int t0 = 0; t0 < k; t0 += 32) {
       const int t = t0 + lane;
       int j[kWarpRows];
+      // asked for before the counts are known; what lies behind is not used
 #pragma unroll
-      for (int u = 0; u < kWarpRows; ++u) {
-        const int mu = __shfl_sync(kAll, m, u);
-        j[u] = u < nrow && t < mu ? __ldg(ix + (int64_t)u * a.C_max + t) : -1;
-      }
+      for (int u = 0; u < kWarpRows; ++u)
+        j[u] = u < nrow && t < min(k, a.C_max - 1)
+                   ? __ldg(ix + (int64_t)u * a.C_max + t)
+                   : -1;
 #pragma unroll
       for (int u = 0; u < kWarpRows; ++u) {
         const int mu = __shfl_sync(kAll, m, u);
         const int lu = __shfl_sync(kAll, last, u);
         if (u < nrow && t < k) {
-          int v = j[u];
+          int v = t < mu ? j[u] : -1;
           if (t < mu && (v < 1 || v > lu)) {  // not a candidate of this row
             raise_flag(a.status, kErrCmax);
             v = -1;
@@ -750,21 +751,32 @@ backward_rows_mma(Args a, int ntile) {
 // ------------------------------------------------------------- column pass
 // A CTA owns 64 keys of one kv head, a warp 16: S^T and dP^T of 16 keys x 16
 // rows at a time, then dV += P^T dO and dK += dS^T Q with P^T and dS^T in two
-// parts straight from their accumulators.  Query rows are staged kRowChunk
-// at a time with their log-sum-exp, D and window, the next chunk (of the
-// group's next head at a head's end) while the current one is used; the
-// listed part is added at the end.
+// parts straight from their accumulators.  Each warp stages its own 16 query
+// rows, with their log-sum-exp, D and window, one block ahead: the warps'
+// bands of rows are shifted against each other, and chunks of rows staged
+// for all of them made each wait, at every chunk, for the one with the most
+// rows in it.  The listed part is added at the end.
 constexpr int kColWarps = 4;
+
+// Rows of D elements without padding: 16-byte piece p of row r stands at
+// place p ^ (r % 8), so that the same piece of eight rows falls on eight
+// different places.
+template <int D>
+struct Swizzled {
+  static constexpr int kRow = D * 2;
+  __device__ __forceinline__ static int at(int r, int p) {
+    return r * kRow + ((p ^ (r & 7)) << 4);
+  }
+};
 
 template <int D, int NP>
 struct ColSmem {
-  static constexpr int RC = kRowChunk;
-  static constexpr int RS = D * 2 + 16;
-  static constexpr size_t keys = (size_t)64 * RS;
-  static constexpr size_t rows = (size_t)RC * RS;
-  // K, V; two buffers of q, the planes of dO, (log-sum-exp, D) and windows
-  static constexpr size_t buffer = (1 + NP) * rows + RC * 12;
-  static constexpr size_t bytes = 2 * keys + 2 * buffer;
+  static constexpr size_t keys = (size_t)64 * D * 2;
+  static constexpr size_t rows = (size_t)16 * D * 2;
+  // of a warp: two buffers of q, the planes of dO, (log-sum-exp, D), windows
+  static constexpr size_t buffer = (1 + NP) * rows + 16 * 12;
+  static constexpr size_t bytes =
+      2 * keys + kColWarps * 2 * buffer + 64 * sizeof(int2);
 };
 
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
@@ -781,73 +793,98 @@ __device__ __forceinline__ void cp_async8(void* dst, const void* src) {
 }
 
 template <int D, int NP>
-__global__ void __launch_bounds__(kColWarps * 32)
+__global__ void __launch_bounds__(kColWarps * 32, D == 64 ? 4 : 2)
 backward_columns_mma(Args a, int ntile) {
   using SM = ColSmem<D, NP>;
-  constexpr int RS = SM::RS, RC = SM::RC;
+  using SW = Swizzled<D>;
   constexpr int KS = D / 16, NT = D / 8;
+  constexpr int kPieces = D * 2 / 16;
   extern __shared__ __align__(16) unsigned char g_smem[];
   chain();
-  unsigned char* sK = g_smem;
-  unsigned char* sV = sK + SM::keys;
-  unsigned char* sB = sV + SM::keys;  // two buffers
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int gr = lane >> 2, tq = lane & 3;
+  unsigned char* sK = g_smem;
+  unsigned char* sV = sK + SM::keys;
+  unsigned char* sB = sV + SM::keys + wid * 2 * SM::buffer;  // the warp's
+  int2* s_span = reinterpret_cast<int2*>(sV + SM::keys +
+                                         kColWarps * 2 * SM::buffer);
   const int L = a.L, nq = a.nq, G = a.Hq / a.Hkv;
   const int seg = blockIdx.x / ntile;
   const int j0 = (blockIdx.x % ntile) * 64;
   const int b = seg / a.Hkv, g = seg % a.Hkv;
   const int kw = j0 + wid * 16;  // the warp's first key
   const float sl2 = kLog2e / sqrtf((float)D), sc = 1.f / sqrtf((float)D);
-  constexpr int kPieces = D * 2 / 16;
-  auto copy_rows = [&](unsigned char* dst, const bf* src, int first, int count,
-                       int limit) {
-    for (int e = threadIdx.x; e < count * kPieces; e += kColWarps * 32) {
-      const int rr = e / kPieces, pc = e % kPieces;
-      cp_async16(dst + rr * RS + pc * 16,
-                 src + (int64_t)min(first + rr, limit - 1) * D + pc * 8);
-    }
-  };
-  // The chunks of rows that see any of the CTA's keys: (head, first row).
-  const int jl = min(j0 + 63, L - 1);  // the CTA's last key
-  const int chunks = (nq + RC - 1) / RC;
-  int hh = -1, rc = 0, rmax = -1;  // head of the group, chunk, its last row
+
+  // K, V and the keys' spans
+  for (int e = threadIdx.x; e < 64 * kPieces; e += kColWarps * 32) {
+    const int rr = e / kPieces, pc = e % kPieces;
+    const int64_t at = ((int64_t)seg * L + min(j0 + rr, L - 1)) * D + pc * 8;
+    cp_async16(sK + SW::at(rr, pc), reinterpret_cast<const bf*>(a.K) + at);
+    cp_async16(sV + SW::at(rr, pc), reinterpret_cast<const bf*>(a.V) + at);
+  }
+  if (threadIdx.x < 64) {
+    if (j0 + threadIdx.x < L)
+      cp_async8(s_span + threadIdx.x,
+                a.span + (int64_t)seg * L + j0 + threadIdx.x);
+    else
+      s_span[threadIdx.x] = make_int2(0, 0);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+
+  // The blocks of 16 rows that may see any of the warp's keys, head by head.
+  const int jl = min(kw + 15, L - 1);  // the warp's last key
+  const int chunks = (nq + kRowChunk - 1) / kRowChunk;
+  int hh = -1, blk = 0, last = -1;    // head of the group, block, last block
+  int lbase = 0, low = 0x7FFFFFFF;    // window starts of chunks lbase + lane
+  if (a.W_i && lane < chunks) low = a.lows[(int64_t)b * chunks + lane];
   auto advance = [&]() {
-    rc += RC;
+    if (kw >= L) return false;
     while (true) {
-      for (; rc <= rmax; rc += RC)
-        if (!a.W_i || a.lows[(int64_t)b * chunks + rc / RC] <= jl) return true;
-      if (++hh >= G) return false;
-      int wm = a.W_i ? a.wmax[b] : (a.W_h ? a.W_h[g * G + hh] : a.W);
-      wm = min(max(wm, 1), L);
-      // rows whose position i has i - wm + 1 <= jl and i >= j0
-      rc = max(j0 - a.p0, 0) / RC * RC;
-      rmax = (int)min((int64_t)jl + wm - 1 - a.p0, (int64_t)nq - 1);
+      while (++blk > last) {
+        if (++hh >= G) return false;
+        int wm = a.W_i ? a.wmax[b] : (a.W_h ? a.W_h[g * G + hh] : a.W);
+        wm = min(max(wm, 1), L);
+        // rows whose position i has i - wm + 1 <= jl and i >= kw
+        blk = max(kw - a.p0, 0) / 16 - 1;
+        const int64_t r1 = min((int64_t)jl + wm - 1 - a.p0, (int64_t)nq - 1);
+        last = r1 < 0 ? -1 : (int)(r1 / 16);
+      }
+      if (!a.W_i) return true;
+      const int c = blk * 16 / kRowChunk;
+      if (c < lbase || c >= lbase + 32) {
+        lbase = c;
+        low = c + lane < chunks ? a.lows[(int64_t)b * chunks + c + lane]
+                                : 0x7FFFFFFF;
+      }
+      if (__shfl_sync(kAll, low, c - lbase) <= jl) return true;
     }
   };
   auto stage = [&](int buf) {
     unsigned char* dst = sB + buf * SM::buffer;
     const int h = g * G + hh;
     const int64_t rowbase = ((int64_t)b * a.Hq + h) * nq;
-    copy_rows(dst, reinterpret_cast<const bf*>(a.Q) + rowbase * D, rc, RC, nq);
+    const bf* Qg = reinterpret_cast<const bf*>(a.Q) + rowbase * D;
 #pragma unroll
-    for (int p = 0; p < NP; ++p)
-      copy_rows(dst + (p + 1) * SM::rows, a.g[p] + rowbase * D, rc, RC, nq);
-    if (threadIdx.x < RC) {
+    for (int e = lane; e < 16 * kPieces; e += 32) {
+      const int rr = e / kPieces, pc = e % kPieces;
+      const int64_t at = (int64_t)min(blk * 16 + rr, nq - 1) * D + pc * 8;
+      cp_async16(dst + SW::at(rr, pc), Qg + at);
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        cp_async16(dst + (p + 1) * SM::rows + SW::at(rr, pc),
+                   a.g[p] + rowbase * D + at);
+    }
+    if (lane < 16) {
       float2* st = reinterpret_cast<float2*>(dst + (1 + NP) * SM::rows);
-      int* sw = reinterpret_cast<int*>(st + RC);
-      const int r = min(rc + (int)threadIdx.x, nq - 1);
-      cp_async8(st + threadIdx.x, a.stats + rowbase + r);
+      int* sw = reinterpret_cast<int*>(st + 16);
+      const int r = min(blk * 16 + lane, nq - 1);
+      cp_async8(st + lane, a.stats + rowbase + r);
       if (a.W_i)
-        cp_async4(sw + threadIdx.x, a.W_i + (int64_t)b * nq + r);
+        cp_async4(sw + lane, a.W_i + (int64_t)b * nq + r);
       else
-        sw[threadIdx.x] = a.W_h ? a.W_h[h] : a.W;
+        sw[lane] = a.W_h ? a.W_h[h] : a.W;
     }
   };
-  copy_rows(sK, reinterpret_cast<const bf*>(a.K) + (int64_t)seg * L * D, j0, 64,
-            L);
-  copy_rows(sV, reinterpret_cast<const bf*>(a.V) + (int64_t)seg * L * D, j0, 64,
-            L);
   float dk[NT][4], dv[NT][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -856,36 +893,35 @@ backward_columns_mma(Args a, int ntile) {
   const int imax = a.p0 + nq - 1;
   bool more = advance();
   if (more) stage(0);
-  asm volatile("cp.async.commit_group;" ::: "memory");
+  asm volatile("cp.async.commit_group;\ncp.async.wait_group 1;" ::: "memory");
+  __syncthreads();  // K, V and the spans are there
 #pragma unroll 1
   for (int buf = 0; more; buf ^= 1) {
-    const int i0 = a.p0 + rc;  // position of the chunk's first row
+    const int i0 = a.p0 + blk * 16;  // position of the block's first row
     more = advance();
     if (more) stage(buf ^ 1);
     asm volatile("cp.async.commit_group;\ncp.async.wait_group 1;" ::: "memory");
-    __syncthreads();
+    __syncwarp();
     const unsigned char* sQ = sB + buf * SM::buffer;
     const unsigned char* sG = sQ + SM::rows;
     const float2* s_st =
         reinterpret_cast<const float2*>(sQ + (1 + NP) * SM::rows);
-    const int* s_w = reinterpret_cast<const int*>(s_st + RC);
-#pragma unroll 1
-    for (int rb = 0; rb < RC; rb += 16) {
-      // do these 16 rows see any, or all, of the warp's 16 keys?
-      const int il = i0 + rb + (lane & 15);
-      const int wl = max(s_w[rb + (lane & 15)], 1);
-      if (!__any_sync(kAll, il >= kw && il <= imax && il - (kw + 15) < wl))
-        continue;
-      const bool inner =
-          __all_sync(kAll, il >= kw + 15 && il <= imax && il - kw < wl);
+    const int* s_w = reinterpret_cast<const int*>(s_st + 16);
+    // do these 16 rows see any, or all, of the warp's 16 keys?
+    const int il = i0 + (lane & 15), wl = max(s_w[lane & 15], 1);
+    const bool any =
+        __any_sync(kAll, il >= kw && il <= imax && il - (kw + 15) < wl);
+    const bool inner =
+        __all_sync(kAll, il >= kw + 15 && il <= imax && il - kw < wl);
+    if (any) {
       float x[2][4], dp[2][4];
-      const int ar = wid * 16 + (lane & 15), ac = (lane >> 4) * 16;
-      const int br = rb + (lane & 7) + ((lane >> 4) << 3);
-      const int bc = ((lane >> 3) & 1) * 16;
+      // places of the operands' pieces: rows of A are keys, of B query rows
+      const int ar = wid * 16 + (lane & 15), ap = lane >> 4;
+      const int br = (lane & 7) + ((lane >> 4) << 3), bp = (lane >> 3) & 1;
       auto step = [&](float (&d)[2][4], const uint32_t (&A)[4],
-                      const unsigned char* bp, bool first) {
+                      const unsigned char* p, bool first) {
         uint32_t f[4];
-        ldsm4(f, bp);
+        ldsm4(f, p);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           if (first) mma0(d[t], A[0], A[1], A[2], A[3], f[2 * t], f[2 * t + 1]);
@@ -894,19 +930,19 @@ backward_columns_mma(Args a, int ntile) {
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t A[4];
-        ldsm4(A, sK + ar * RS + ks * 32 + ac);
-        step(x, A, sQ + br * RS + ks * 32 + bc, ks == 0);
-        ldsm4(A, sV + ar * RS + ks * 32 + ac);
+        ldsm4(A, sK + SW::at(ar, 2 * ks + ap));
+        step(x, A, sQ + SW::at(br, 2 * ks + bp), ks == 0);
+        ldsm4(A, sV + SW::at(ar, 2 * ks + ap));
 #pragma unroll
         for (int p = 0; p < NP; ++p)
-          step(dp, A, sG + p * SM::rows + br * RS + ks * 32 + bc,
+          step(dp, A, sG + p * SM::rows + SW::at(br, 2 * ks + bp),
                ks == 0 && p == 0);
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int rl = rb + 8 * t + 2 * tq + c;
+          const int rl = 8 * t + 2 * tq + c;
           const float2 st = s_st[rl];
           const int i = i0 + rl, w = max(s_w[rl], 1);
 #pragma unroll
@@ -927,18 +963,18 @@ backward_columns_mma(Args a, int ntile) {
         split2(dp[c >> 1][(c & 1) * 2], dp[c >> 1][(c & 1) * 2 + 1], &dh[c],
                &dl[c]);
       }
-      const int tr = (rb + (lane & 15)) * RS + (lane >> 4) * 16;
+      const int tr = lane & 15, tp = lane >> 4;
 #pragma unroll
       for (int t = 0; t < NT; t += 2) {
         uint32_t f[4];
-        ldsm4t(f, sQ + tr + t * 16);
+        ldsm4t(f, sQ + SW::at(tr, t + tp));
         mma(dk[t], dh[0], dh[1], dh[2], dh[3], f[0], f[1]);
         mma(dk[t + 1], dh[0], dh[1], dh[2], dh[3], f[2], f[3]);
         mma(dk[t], dl[0], dl[1], dl[2], dl[3], f[0], f[1]);
         mma(dk[t + 1], dl[0], dl[1], dl[2], dl[3], f[2], f[3]);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          ldsm4t(f, sG + p * SM::rows + tr + t * 16);
+          ldsm4t(f, sG + p * SM::rows + SW::at(tr, t + tp));
           mma(dv[t], ph[0], ph[1], ph[2], ph[3], f[0], f[1]);
           mma(dv[t + 1], ph[0], ph[1], ph[2], ph[3], f[2], f[3]);
           if (p == 0) {  // lo x lo is below what two parts keep
@@ -948,60 +984,98 @@ backward_columns_mma(Args a, int ntile) {
         }
       }
     }
-    __syncthreads();  // the buffer may be written again
+    __syncwarp();  // the buffer may be written again
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");  // K and V, if unused
-  __syncthreads();
-  // The listed part: a key's first range (`top`) and the later ranges'
-  // shares (`carry`).  Up to kShort shares are added by the lanes that hold
-  // the key; longer runs (the anchor's spans nq G / kRange ranges) first by
-  // the whole CTA, in a fixed order.
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  // The listed part.  A key's is the sum of rows [dK | dV]: one from its
+  // first range (`top`), then the later ranges' shares (`carry`).  Up to
+  // kShort rows are added by the lanes that hold the key, eight keys side by
+  // side.  For keys with more (the first of a long sequence, which most rows
+  // had to choose from, and the anchor) the warp takes the rows as one
+  // sequence, some on their way, a row across its lanes, whole blocks by
+  // their sum, and leaves each key's total in shared memory (its row buffers
+  // are free now).
+  __syncwarp();
   constexpr int kShort = 4;
-  constexpr int kCols = 2 * D / 4, kParts = kColWarps * 32 / kCols;
-  int2* s_span = reinterpret_cast<int2*>(sB);
-  float4* s_sum = reinterpret_cast<float4*>(sB + 64 * 8);  // [parts][2 D]
-  if (threadIdx.x < 64)
-    s_span[threadIdx.x] = j0 + threadIdx.x < L
-                              ? a.span[(int64_t)seg * L + j0 + threadIdx.x]
-                              : make_int2(0, 0);
-  __syncthreads();
+  auto rows_of = [&](const int2& sp) {
+    return sp.y > sp.x ? (sp.y - 1) / kRange - sp.x / kRange + 1 : 0;
+  };
+  constexpr int kRow = 2 * D + 4;  // floats; padded against bank conflicts
+  static_assert(16 * kRow * 4 <= 2 * (int)SM::buffer, "sums fit the buffers");
+  constexpr int NV = 2 * D / 128;  // float4 per lane and row
+  float* sums = reinterpret_cast<float*>(sB);
+  if (__any_sync(kAll, rows_of(s_span[wid * 16 + (lane & 15)]) > kShort)) {
+    const float* carry = a.carry + (int64_t)seg * a.w.ranges * 2 * D;
+    const float* bsum = a.bsum + (int64_t)seg * a.w.blocks * 2 * D;
+    const int64_t col = (int64_t)seg * L + kw;
+    const int pb = a.w.per_block;
+    int key = -1, r = 0, e = -1, k1 = 0;  // next row: range r of key, to e
+    int2 sp = make_int2(0, 0);
+    // the next row's place; nullptr behind the last
+    auto next = [&](int* of) -> const float* {
+      if (r > e) {  // the next long key
+        do {
+          if (++key >= 16) return nullptr;
+          sp = s_span[wid * 16 + key];
+        } while (rows_of(sp) <= kShort);
+        r = sp.x / kRange;
+        e = (sp.y - 1) / kRange;
+        k1 = sp.y / (pb * kRange);  // behind its last whole block
+        *of = key;
+        ++r;
+        return a.top + (col + key) * 2 * D;
+      }
+      *of = key;
+      if (r % pb == 0 && r / pb < k1) {
+        r += pb;
+        return bsum + (int64_t)(r / pb - 1) * 2 * D;
+      }
+      return carry + (int64_t)r++ * 2 * D;
+    };
+    constexpr int U = D == 64 ? 4 : 8;
+    float4 x[U][NV], sum[NV];
+    int cur = -1;
+    bool more_rows = true;
 #pragma unroll 1
-  for (int kl = 0; kl < 64; ++kl) {
-    const int2 sp = s_span[kl];
-    const int f = sp.x / kRange, e = (sp.y - 1) / kRange;
-    if (sp.y <= sp.x || e - f <= kShort) continue;  // the same for the CTA
-    const int c4 = threadIdx.x % kCols, part = threadIdx.x / kCols;
-    const float4* p = reinterpret_cast<const float4*>(
-                          a.carry + (int64_t)seg * a.w.ranges * 2 * D) + c4;
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int r = f + 1 + part; r <= e; r += kParts) {
-      const float4 v = p[(int64_t)r * kCols];
-      t.x += v.x;
-      t.y += v.y;
-      t.z += v.z;
-      t.w += v.w;
+    while (more_rows) {
+      int of[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        of[u] = -1;
+        const float* p = more_rows ? next(&of[u]) : nullptr;
+        more_rows = p != nullptr;
+        if (p)
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+            x[u][v] = reinterpret_cast<const float4*>(p)[32 * v + lane];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (of[u] != cur) {
+          if (cur >= 0)
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+              reinterpret_cast<float4*>(sums + cur * kRow)[32 * v + lane] =
+                  sum[v];
+          cur = of[u];
+#pragma unroll
+          for (int v = 0; v < NV; ++v) sum[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (of[u] < 0) break;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          sum[v].x += x[u][v].x;
+          sum[v].y += x[u][v].y;
+          sum[v].z += x[u][v].z;
+          sum[v].w += x[u][v].w;
+        }
+      }
     }
-    s_sum[part * kCols + c4] = t;
-    __syncthreads();
-    if (kl >> 4 == wid && (kl & 7) == gr) {
-      const float* q = reinterpret_cast<const float*>(s_sum) + 2 * tq;
-      const int u = (kl >> 3) & 1;
+    if (cur >= 0)
 #pragma unroll
-      for (int part2 = 0; part2 < kParts; ++part2)
-#pragma unroll
-        for (int t2 = 0; t2 < NT; ++t2)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float k2 = q[part2 * 2 * D + 8 * t2 + c];
-            const float v2 = q[part2 * 2 * D + D + 8 * t2 + c];
-            dk[t2][c] += u ? 0.f : k2;
-            dk[t2][2 + c] += u ? k2 : 0.f;
-            dv[t2][c] += u ? 0.f : v2;
-            dv[t2][2 + c] += u ? v2 : 0.f;
-          }
-    }
-    __syncthreads();
+      for (int v = 0; v < NV; ++v)
+        reinterpret_cast<float4*>(sums + cur * kRow)[32 * v + lane] = sum[v];
+    __syncwarp();
   }
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -1009,24 +1083,26 @@ backward_columns_mma(Args a, int ntile) {
     if (j >= L) continue;
     const int64_t col = (int64_t)seg * L + j;
     const int2 sp = s_span[wid * 16 + gr + 8 * u];
-    if (sp.y > sp.x) {
-      const int f = sp.x / kRange, e = (sp.y - 1) / kRange;
-      const int r1 = e - f > kShort ? f : e;
-      for (int r = f; r <= r1; ++r) {
-        const float* p =
-            (r == f ? a.top + col * 2 * D
-                    : a.carry + ((int64_t)seg * a.w.ranges + r) * 2 * D) +
-            2 * tq;
+    const int n = rows_of(sp), f = sp.x / kRange;
+    auto add = [&](const float* p) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float2 k2 = *reinterpret_cast<const float2*>(p + 8 * t);
-          const float2 v2 = *reinterpret_cast<const float2*>(p + D + 8 * t);
-          dk[t][2 * u] += k2.x;
-          dk[t][2 * u + 1] += k2.y;
-          dv[t][2 * u] += v2.x;
-          dv[t][2 * u + 1] += v2.y;
-        }
+      for (int t = 0; t < NT; ++t) {
+        const float2 k2 = *reinterpret_cast<const float2*>(p + 8 * t);
+        const float2 v2 = *reinterpret_cast<const float2*>(p + D + 8 * t);
+        dk[t][2 * u] += k2.x;
+        dk[t][2 * u + 1] += k2.y;
+        dv[t][2 * u] += v2.x;
+        dv[t][2 * u + 1] += v2.y;
       }
+    };
+    if (n > kShort) {
+      add(sums + (gr + 8 * u) * kRow + 2 * tq);
+    } else {
+      for (int r = 0; r < n; ++r)
+        add((r == 0 ? a.top + col * 2 * D
+                    : a.carry +
+                          ((int64_t)seg * a.w.ranges + f + r) * 2 * D) +
+            2 * tq);
     }
     uint32_t* ok = reinterpret_cast<uint32_t*>(
         reinterpret_cast<bf*>(a.dK) + col * D + 2 * tq);

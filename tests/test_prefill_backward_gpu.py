@@ -66,6 +66,7 @@ CASES = [
     (1, 700, 700, 4, 2, 64, 64, 32, BF, BF),
     (1, 257, 900, 2, 1, 128, 256, 100, BF, BF),
     (1, 64, 70000, 2, 1, 64, 64, 32, BF, BF),
+    (1, 300, 70000, 2, 1, 64, 64, 32, BF, BF),   # three sort passes
     (1, 250, 300, 2, 1, 64, 20, 17, F32, BF),
 ]
 IDS = lambda c: "-".join(str(x).replace("torch.", "") for x in c)  # noqa: E731
@@ -295,6 +296,23 @@ def test_decode_from_projection_rows():
                                                V, W, k)
     assert torch.equal(idx, idx2[:, :, 0]) and torch.equal(cnt, cnt2[:, :, 0])
     assert (o - O[:, :, 0]).abs().max() <= 1e-2
+
+
+@pytest.mark.parametrize("dt,d,nq,W,k", [
+    (BF, 64, 700, 64, 32), (BF, 128, 300, 40, 64), (F32, 64, 300, 20, 16)])
+def test_debug_build(dt, d, nq, W, k):
+    """The index-checking build: no check fires, and equal bits."""
+    from sparse_transformer_attention_b200 import binding, build
+    x = make(1, nq, nq, 4, 2, d, dt, dt, popular=8, scale=0.5)
+    idx, cnt, want = run(*x, W, k)
+    prev = binding.use_library(build.build(debug=True))
+    try:
+        assert binding.load().condensate_attn_build_flags() == 1
+        idx2, cnt2, got = run(*x, W, k)  # asserts a clean status word
+    finally:
+        binding.use_library(prev)
+    assert torch.equal(idx, idx2) and torch.equal(cnt, cnt2)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
 def test_refusals():
