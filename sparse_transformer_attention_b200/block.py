@@ -9,9 +9,13 @@ the gradients.  norm_rope, attention and qkv_attention are the same
 operators under torch.autograd.
 
 As in `binding`, this module marshals arguments; the computation runs in the
-library's kernels.  Calls run on the device of their tensors, on `stream` (by
-default that device's current stream), and wait for nothing, so they can be
-captured into CUDA graphs.
+library's kernels.  The condensate_attn_* calls here run on the device of
+their tensors, on `stream` (by default that device's current stream), and
+wait for nothing, so they can be captured into CUDA graphs.  (Under autograd
+the forward pass with W_i or W_h reads the largest window back to the host,
+as condensate_attn_prefill does, and cannot; and PyTorch does not allow a
+captured backward pass while a graph of the same leaves, built outside the
+capture, is alive.)
 """
 from __future__ import annotations
 
@@ -22,45 +26,37 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding
-from .binding import _check, _dt, _ptr, _require
+from .binding import _check, _dt, _require
 
-_DTYPES = (torch.float32, torch.bfloat16)
+_DT = {torch.float32: binding.CA_F32, torch.bfloat16: binding.CA_BF16}
 
 
+# torch.cuda.current_stream(dev).cuda_stream and torch.cuda.current_device()
+# without the objects and checks around them, which a decode would feel
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_device = torch._C._cuda_getDevice
 
 
-class _On:
-    """`dev` current, and what is allocated inside belonging to `stream`; as
-    a value, the raw stream to launch on."""
-    __slots__ = ("raw", "guard")
+def _elsewhere(dev: torch.device, stream) -> bool:
+    """Whether a call on tensors of `dev` needs another device or stream than
+    the current ones (then it repeats itself inside `_on`)."""
+    return stream is not None or _device() != dev.index
 
-    def __init__(self, dev: torch.device, stream):
-        self.guard = None
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError(
-                    f"stream is on {stream.device}, tensors on {dev}")
-            self.guard = torch.cuda.stream(stream)
-            self.raw = stream.cuda_stream
-        else:
-            if torch.cuda.current_device() != dev.index:
-                self.guard = torch.cuda.device(dev)
-            # torch.cuda.current_stream(dev).cuda_stream without the object
-            self.raw = _raw_stream(dev.index)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.raw
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _on(dev: torch.device, stream):
+    """`dev` current and, if given, `stream`: what is allocated inside
+    belongs to it."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, tensors on {dev}")
+    return torch.cuda.stream(stream)
 
 
 def _expect(t: torch.Tensor, name: str, shape, dtype, dev):
     """Shape, type and device of one argument."""
+    if t.shape == shape and t.dtype is dtype and t.device == dev:
+        return
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, "
                          f"got {tuple(t.shape)}")
@@ -73,6 +69,20 @@ def _expect(t: torch.Tensor, name: str, shape, dtype, dev):
 def _dense(t: torch.Tensor, name: str, shape, dtype, dev):
     _expect(t, name, shape, dtype, dev)
     _require(t, name)
+
+
+def _address(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _bytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _workspace(t: torch.Tensor, dev):
+    _require(t, "workspace")
+    if t.device != dev:
+        raise ValueError(f"workspace is on {t.device}, expected {dev}")
 
 
 # ca_rows[3] and ca_norm_rope of the header as packed bytes (a third of the
@@ -109,28 +119,41 @@ def _head_major(t: Optional[torch.Tensor], name: str, B: int, n: int, H: int):
 def _rope_params(d, n_tokens, dev, inv_freq, q_weight, k_weight, eps,
                  positions, pos0, interleaved) -> bytes:
     w_dtype = None
-    for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            if w.dtype not in _DTYPES or (w_dtype not in (None, w.dtype)):
-                raise TypeError("q_weight and k_weight must both be float32 "
-                                "or both bfloat16")
-            w_dtype = w.dtype
-            _dense(w, nm, (d,), None, dev)
-    rot = 0
+    qw = kw = fq = ps = rot = 0
+    if q_weight is not None:
+        w_dtype = q_weight.dtype
+        _dense(q_weight, "q_weight", (d,), w_dtype, dev)
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        w_dtype = w_dtype or k_weight.dtype
+        _dense(k_weight, "k_weight", (d,), w_dtype, dev)
+        kw = k_weight.data_ptr()
+    if w_dtype is not None and w_dtype not in _DT:
+        raise TypeError("q_weight and k_weight must be float32 or bfloat16")
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
         _dense(inv_freq, "inv_freq", (rot // 2,), torch.float32, dev)
+        fq = inv_freq.data_ptr()
     if positions is not None:
         _dense(positions, "positions", n_tokens, torch.int32, dev)
+        ps = positions.data_ptr()
     if not -(1 << 31) <= pos0 < 1 << 31:
         raise ValueError("pos0 must fit 32 bits")
-    return _PARAMS.pack(
-        0 if q_weight is None else q_weight.data_ptr(),
-        0 if k_weight is None else k_weight.data_ptr(),
-        binding.CA_BF16 if w_dtype is torch.bfloat16 else binding.CA_F32,
-        eps, 0 if inv_freq is None else inv_freq.data_ptr(), rot,
-        1 if interleaved else 0,
-        0 if positions is None else positions.data_ptr(), pos0)
+    return _PARAMS.pack(qw, kw, _DT[w_dtype] if w_dtype is not None else 0,
+                        eps, fq, rot, 1 if interleaved else 0, ps, pos0)
+
+
+def _out(y: Optional[torch.Tensor], x: Optional[torch.Tensor], name: str,
+         shape, dtype, dev):
+    """The tensor a result goes to: y, or a new one beside x."""
+    if x is None:
+        if y is not None:
+            raise ValueError(f"{name} given without its input")
+        return None
+    if y is None:
+        return x.new_empty(shape)
+    _expect(y, name, shape, dtype, dev)
+    return y
 
 
 def _sizes(q, k, v):
@@ -171,31 +194,30 @@ def condensate_attn_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor],
     Returns (Q, K, V).
     """
     B, n, Hq, Hkv, d = _sizes(q, k, v)
-    dev = q.device
+    dt, dev = q.dtype, q.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return condensate_attn_norm_rope(q, k, v, inv_freq, q_weight,
+                                             k_weight, eps, positions, pos0,
+                                             interleaved, Q, K, V)
     par = _rope_params(d, (B, n), dev, inv_freq, q_weight, k_weight, eps,
                        positions, pos0, interleaved)
-    with _On(dev, stream) as s:
-        outs = []
-        for x, y, H, nm in ((q, Q, Hq, "Q"), (k, K, Hkv, "K"),
-                            (v, V, Hkv, "V")):
-            if x is None:
-                if y is not None:
-                    raise ValueError(f"{nm} given without its input")
-            elif y is None:
-                y = x.new_empty((B, H, n, d))
-            else:
-                _expect(y, nm, (B, H, n, d), q.dtype, dev)
-            outs.append(y)
-        code = binding.load().condensate_attn_norm_rope(
-            _ROWS3.pack(*_token_major(q, "q", B, n, Hq),
-                        *_token_major(k, "k", B, n, Hkv),
-                        *_token_major(v, "v", B, n, Hkv)),
-            _dt(q.dtype), B, n, Hq, Hkv, d, par,
-            _ROWS3.pack(*_head_major(outs[0], "Q", B, n, Hq),
-                        *_head_major(outs[1], "K", B, n, Hkv),
-                        *_head_major(outs[2], "V", B, n, Hkv)), s)
-    _check(code, "condensate_attn_norm_rope")
-    return tuple(outs)
+    kv = (B, Hkv, n, d)
+    Q = _out(Q, q, "Q", (B, Hq, n, d), dt, dev)
+    K = _out(K, k, "K", kv, dt, dev)
+    V = _out(V, v, "V", kv, dt, dev)
+    code = binding.load().condensate_attn_norm_rope(
+        _ROWS3.pack(*_token_major(q, "q", B, n, Hq),
+                    *_token_major(k, "k", B, n, Hkv),
+                    *_token_major(v, "v", B, n, Hkv)),
+        _dt(dt), B, n, Hq, Hkv, d, par,
+        _ROWS3.pack(*_head_major(Q, "Q", B, n, Hq),
+                    *_head_major(K, "K", B, n, Hkv),
+                    *_head_major(V, "V", B, n, Hkv)),
+        _raw_stream(dev.index))
+    if code:
+        _check(code, "condensate_attn_norm_rope")
+    return Q, K, V
 
 
 def condensate_attn_norm_rope_backward(
@@ -232,48 +254,50 @@ def condensate_attn_norm_rope_backward(
             if t is None:
                 raise ValueError(f"{nm} is needed for the norm's gradient")
             _expect(t, nm, (B, n, H, d), dt, dev)
-    q, k = q if q_weight is not None else None, \
-        k if k_weight is not None else None
+    if q_weight is None:
+        q = None
+    if k_weight is None:
+        k = None
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return condensate_attn_norm_rope_backward(
+                dQ, dK, dV, q, k, inv_freq, q_weight, k_weight, eps,
+                positions, pos0, interleaved, dq, dk, dv, weight_grads,
+                workspace)
     par = _rope_params(d, (B, n), dev, inv_freq, q_weight, k_weight, eps,
                        positions, pos0, interleaved)
-    with _On(dev, stream) as s:
-        outs = []
-        for g, x, H, nm in ((dQ, dq, Hq, "dq"), (dK, dk, Hkv, "dk"),
-                            (dV, dv, Hkv, "dv")):
-            if g is None:
-                if x is not None:
-                    raise ValueError(f"{nm} given without its gradient")
-            elif x is None:
-                x = g.new_empty((B, n, H, d))
-            else:
-                _expect(x, nm, (B, n, H, d), dt, dev)
-            outs.append(x)
-        dqw = torch.empty_like(q_weight) \
-            if weight_grads and q_weight is not None else None
-        dkw = torch.empty_like(k_weight) \
-            if weight_grads and k_weight is not None else None
-        lib = binding.load()
-        if (dqw is not None or dkw is not None) and workspace is None:
-            workspace = torch.empty(
-                lib.condensate_attn_norm_rope_workspace_size(d),
-                dtype=torch.uint8, device=dev)
-        if workspace is not None:
-            _require(workspace, "workspace")
-        code = lib.condensate_attn_norm_rope_backward(
-            _ROWS3.pack(*_head_major(dQ, "dQ", B, n, Hq),
-                        *_head_major(dK, "dK", B, n, Hkv),
-                        *_head_major(dV, "dV", B, n, Hkv)),
-            _ROWS3.pack(*_token_major(q, "q", B, n, Hq),
-                        *_token_major(k, "k", B, n, Hkv), *_NONE),
-            _dt(dt), B, n, Hq, Hkv, d, par,
-            _ROWS3.pack(*_token_major(outs[0], "dq", B, n, Hq),
-                        *_token_major(outs[1], "dk", B, n, Hkv),
-                        *_token_major(outs[2], "dv", B, n, Hkv)),
-            _ptr(dqw), _ptr(dkw), _ptr(workspace),
-            0 if workspace is None else workspace.numel() *
-            workspace.element_size(), s)
-    _check(code, "condensate_attn_norm_rope_backward")
-    return (*outs, dqw, dkw)
+    kv = (B, n, Hkv, d)
+    dq = _out(dq, dQ, "dq", (B, n, Hq, d), dt, dev)
+    dk = _out(dk, dK, "dk", kv, dt, dev)
+    dv = _out(dv, dV, "dv", kv, dt, dev)
+    dqw = dkw = None
+    if weight_grads:
+        if q_weight is not None:
+            dqw = torch.empty_like(q_weight)
+        if k_weight is not None:
+            dkw = torch.empty_like(k_weight)
+    lib = binding.load()
+    if workspace is not None:
+        _workspace(workspace, dev)
+    elif dqw is not None or dkw is not None:
+        workspace = torch.empty(
+            lib.condensate_attn_norm_rope_workspace_size(d),
+            dtype=torch.uint8, device=dev)
+    code = lib.condensate_attn_norm_rope_backward(
+        _ROWS3.pack(*_head_major(dQ, "dQ", B, n, Hq),
+                    *_head_major(dK, "dK", B, n, Hkv),
+                    *_head_major(dV, "dV", B, n, Hkv)),
+        _ROWS3.pack(*_token_major(q, "q", B, n, Hq),
+                    *_token_major(k, "k", B, n, Hkv), *_NONE),
+        _dt(dt), B, n, Hq, Hkv, d, par,
+        _ROWS3.pack(*_token_major(dq, "dq", B, n, Hq),
+                    *_token_major(dk, "dk", B, n, Hkv),
+                    *_token_major(dv, "dv", B, n, Hkv)),
+        _address(dqw), _address(dkw), _address(workspace), _bytes(workspace),
+        _raw_stream(dev.index))
+    if code:
+        _check(code, "condensate_attn_norm_rope_backward")
+    return dq, dk, dv, dqw, dkw
 
 
 def condensate_attn_prefill_backward_workspace_size(
@@ -316,32 +340,40 @@ def condensate_attn_prefill_backward(
         _dense(W_i, "W_i", (B, nq), torch.int32, dev)
     if W_h is not None:
         _dense(W_h, "W_h", (Hq,), torch.int32, dev)
-    with _On(dev, stream) as s:
-        if dQ is None:
-            dQ = torch.empty_like(Q)
-        else:
-            _dense(dQ, "dQ", Q.shape, dt, dev)
-        if dK is None:
-            dK = torch.empty_like(K)
-        else:
-            _dense(dK, "dK", K.shape, dt, dev)
-        if dV is None:
-            dV = torch.empty_like(V)
-        else:
-            _dense(dV, "dV", V.shape, dt, dev)
-        if workspace is None:
-            workspace = torch.empty(
-                condensate_attn_prefill_backward_workspace_size(
-                    dt, dO.dtype, B, nq, L, Hq, Hkv, d, k),
-                dtype=torch.uint8, device=dev)
-        _require(workspace, "workspace")
-        code = binding.load().condensate_attn_prefill_backward(
-            Q.data_ptr(), K.data_ptr(), V.data_ptr(), _dt(dt), dO.data_ptr(),
-            _dt(dO.dtype), B, nq, L, Hq, Hkv, d, int(W), int(k), _ptr(W_i),
-            _ptr(W_h), idx.data_ptr(), idx_count.data_ptr(), idx.shape[-1],
-            dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), s)
-    _check(code, "condensate_attn_prefill_backward")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return condensate_attn_prefill_backward(
+                Q, K, V, dO, idx, idx_count, W, k, W_i, W_h, dQ, dK, dV,
+                workspace)
+    if dQ is None:
+        dQ = torch.empty_like(Q)
+    else:
+        _dense(dQ, "dQ", Q.shape, dt, dev)
+    if dK is None:
+        dK = torch.empty_like(K)
+    else:
+        _dense(dK, "dK", K.shape, dt, dev)
+    if dV is None:
+        dV = torch.empty_like(V)
+    else:
+        _dense(dV, "dV", V.shape, dt, dev)
+    dtype, o_dtype = _dt(dt), _dt(dO.dtype)
+    lib = binding.load()
+    if workspace is not None:
+        _workspace(workspace, dev)
+    else:
+        workspace = torch.empty(
+            lib.condensate_attn_prefill_backward_workspace_size(
+                dtype, o_dtype, B, nq, L, Hq, Hkv, d, k),
+            dtype=torch.uint8, device=dev)
+    code = lib.condensate_attn_prefill_backward(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), dtype, dO.data_ptr(),
+        o_dtype, B, nq, L, Hq, Hkv, d, int(W), int(k), _address(W_i),
+        _address(W_h), idx.data_ptr(), idx_count.data_ptr(), idx.shape[-1],
+        dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), workspace.data_ptr(),
+        _bytes(workspace), _raw_stream(dev.index))
+    if code:
+        _check(code, "condensate_attn_prefill_backward")
     return dQ, dK, dV
 
 

@@ -1,12 +1,14 @@
-// The prefill's backward pass for bf16 on matrix instructions.  All products
-// run as m16n8k16 bf16 with fp32 sums.  Operands that are not inputs (p, dS,
-// e dP) enter in two bf16 parts, hi + lo, so that they keep 16 bits: with one
-// part the gradients' error would be half as large again as that of the
-// rounding to bf16 at the end.
+// The row and the column pass of the prefill's backward for bf16, on matrix
+// instructions: m16n8k16 bf16 with fp32 sums.  Operands that are not inputs
+// (p, dS, e dP) enter in two bf16 parts, hi + lo, so that they keep 16 bits:
+// one part's rounding, of the size of the gradients' own at the end, would
+// make their error about 1.4 times as large.
 //
-// The work per (row, key) pair is small and most pairs are gathered, so what
-// bounds these kernels is reading rows from L2 and issuing instructions, not
-// the tensor pipe; the layouts below keep both low.
+// The work per (row, key) pair is small and a third of the pairs are
+// gathered, 16 rows that no other query shares, so what bounds these kernels
+// is reading rows from L2 and issuing instructions, not the tensor pipe (18
+// to 28% of its cycles): an operand of one tcgen05 product would be 128 rows
+// that have to stand in shared memory first, for one useful column.
 #include "../launch.cuh"
 #include "backward.cuh"
 
@@ -103,6 +105,13 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t* hi,
 // phase goes through the chunks backwards, starting with the two that are
 // still there.  Two warps share 16 rows: in the window each takes every
 // second block of keys, in the Top-k eight rows.
+//
+// Measured: 196608 rows of 64 + 32 keys, d = 64: 289 us, of which a CTA's 64
+// rows spend 16% on the index rows, 10% and 16% on the window's two passes and
+// 56% on the Top-k (68 GB/s per SM, about half of what its L2 port carries);
+// without Top-k keys it is 150 us, each 16 more of them 70 us.  65536 rows of
+// 64 to 256 + 64 keys, d = 128: 386 us.  Three CTAs of 80 registers per SM
+// instead of two of 128 were slower (352 us at d = 64).
 constexpr int kRowWarps = 8;
 constexpr int kWarpRows = 64 / kRowWarps;  // Top-k rows of a warp
 
@@ -756,6 +765,11 @@ backward_rows_mma(Args a, int ntile) {
 // bands of rows are shifted against each other, and chunks of rows staged
 // for all of them made each wait, at every chunk, for the one with the most
 // rows in it.  The listed part is added at the end.
+//
+// Measured: 196608 keys seen by 64 rows each, d = 64: 118 us; 32768 keys seen
+// by 2 x 160 rows, d = 128: 162 us.  Bound by latency and issue at four (two)
+// warps per scheduler; two warps per 16 keys, one for each gradient, doubled
+// the warps and computed S^T twice: 174 and 237 us.
 constexpr int kColWarps = 4;
 
 // Rows of D elements without padding: 16-byte piece p of row r stands at

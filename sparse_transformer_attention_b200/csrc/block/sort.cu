@@ -4,10 +4,10 @@
 // (sort_count), scans every digit's counts over the tiles (sort_scan) and
 // places the entries (sort_place), which first orders its tile in shared
 // memory so that what it writes is runs of consecutive places: with entries
-// written where they stood, 32 lanes hit 32 sectors and a pass of the 8K
-// GPT-2-small case took 100 us.  Lists of one tile or a few (up to kSmall
+// written where they stood, 32 lanes hit 32 sectors and placing 6.5 M entries
+// took 118 us where it takes 49.  Lists of one tile or a few (up to kSmall
 // entries) are sorted by one CTA each in shared memory, in one launch
-// instead of six.
+// instead of six (8704 entries: 18 us instead of 40).
 #include "../launch.cuh"
 #include "backward.cuh"
 
