@@ -188,6 +188,30 @@ def test_gradients_against_differences():
         assert abs(num - ana) <= 1e-5 * (grad.double() * u).abs().sum()
 
 
+def test_offsets_beyond_32_bits():
+    """180,000 tokens of 96 heads x 128: the last tokens lie behind element
+    2^31 of the projection."""
+    n, Hq, Hkv, d = 180_000, 32, 32, 128
+    x = torch.empty(1, n, Hq + 2 * Hkv, d, dtype=BF, device="cuda").normal_()
+    w = torch.ones(d, dtype=BF, device="cuda")
+    inv = 10000.0 ** (-torch.arange(0, d, 2, device="cuda") / d)
+    q, k, v = x[:, :, :Hq], x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:]
+    Q, K, V = ca.condensate_attn_norm_rope(q, k, v, inv, w, w)
+    dq, dk, dv, _, _ = ca.condensate_attn_norm_rope_backward(
+        Q, K, V, q, k, inv, w, w)
+    at = slice(n - 40, n)
+    pos = torch.arange(n - 40, n, device="cuda").view(1, 40)
+    ang = plain.angles(pos, inv)
+    for a, A, da in ((q, Q, dq), (k, K, dk)):
+        plain.check(A[:, :, at], *plain.norm_rope(a[:, at], w, 1e-6, ang,
+                                                  False))
+        dx, bx, _, _ = plain.norm_rope_backward(A[:, :, at], a[:, at], w,
+                                                1e-6, ang, False, 1)
+        plain.check(da[:, at], dx, bx)
+    assert torch.equal(V[:, :, at], v[:, at].transpose(1, 2))
+    assert torch.equal(dv[:, at], v[:, at])
+
+
 def test_equal_bits_streams_and_graphs():
     """The same call twice, on a side stream, and captured and replayed with
     new inputs in the same buffers."""

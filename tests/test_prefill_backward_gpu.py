@@ -298,6 +298,41 @@ def test_decode_from_projection_rows():
     assert (o - O[:, :, 0]).abs().max() <= 1e-2
 
 
+def test_offsets_beyond_32_bits():
+    """8 kv heads x 2.1 M keys x 128: the last head's rows lie behind element
+    2^31.  The sets are made here; the last head is compared whole, at the
+    keys that its rows list and see."""
+    H, L, nq, d, W, k = 8, 2_100_000, 16, 128, 16, 8
+    g = torch.Generator(device="cuda").manual_seed(6)
+    K, V = (torch.empty(1, H, L, d, dtype=BF, device="cuda").normal_(
+        generator=g) for _ in range(2))
+    Q, dO = (torch.randn(1, H, nq, d, generator=g, device="cuda").to(BF)
+             for _ in range(2))
+    far = torch.randint(1, L - nq - W, (1, H, nq, k), generator=g,
+                        device="cuda")
+    far[..., 0] = L - nq - W - 1  # every row's
+    far = far.sort(-1).values
+    i = torch.arange(L - nq, L, device="cuda").view(1, 1, nq, 1)
+    win = (i - W + 1 + torch.arange(W, device="cuda")).expand(1, H, nq, W)
+    idx = torch.cat([torch.zeros_like(far[..., :1]), far, win],
+                    -1).to(torch.int32).contiguous()
+    cnt = torch.full((1, H, nq), 1 + k + W, dtype=torch.int32, device="cuda")
+    dQ, dK, dV = ca.condensate_attn_prefill_backward(Q, K, V, dO, idx, cnt, W,
+                                                     k)
+    # the listed and seen keys of the last head, and the sets over them
+    keys = torch.unique(idx[0, -1].long())
+    at = torch.searchsorted(keys, idx[:, -1:].long())
+    part = lambda t: t[:, -1:, keys].contiguous()  # noqa: E731
+    last = lambda t: t[:, -1:]  # noqa: E731
+    want = plain.attention_backward(last(Q), part(K), part(V), last(dO), at)
+    got = last(dQ), part(dK), part(dV)
+    for x, (y, b), nm in zip(got, want, ("dQ", "dK", "dV")):
+        plain.check(x, y, b, nm)
+    other = torch.ones(L, dtype=torch.bool, device="cuda")
+    other[keys] = False
+    assert not dK[0, -1][other].any() and not dV[0, -1][other].any()
+
+
 @pytest.mark.parametrize("dt,d,nq,W,k", [
     (BF, 64, 700, 64, 32), (BF, 128, 300, 40, 64), (F32, 64, 300, 20, 16)])
 def test_debug_build(dt, d, nq, W, k):
