@@ -783,14 +783,17 @@ struct Swizzled {
   }
 };
 
-template <int D, int NP>
+// SPLIT: the CTA's four warps share 16 keys instead, a block of rows each in
+// turn, and their sums meet at the end, in the warps' order.
+template <int D, int NP, bool SPLIT>
 struct ColSmem {
-  static constexpr size_t keys = (size_t)64 * D * 2;
+  static constexpr int kKeys = SPLIT ? 16 : 64;
+  static constexpr size_t keys = (size_t)kKeys * D * 2;
   static constexpr size_t rows = (size_t)16 * D * 2;
   // of a warp: two buffers of q, the planes of dO, (log-sum-exp, D), windows
   static constexpr size_t buffer = (1 + NP) * rows + 16 * 12;
   static constexpr size_t bytes =
-      2 * keys + kColWarps * 2 * buffer + 64 * sizeof(int2);
+      2 * keys + kColWarps * 2 * buffer + kKeys * sizeof(int2);
 };
 
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
@@ -806,10 +809,11 @@ __device__ __forceinline__ void cp_async8(void* dst, const void* src) {
                : "memory");
 }
 
-template <int D, int NP>
+template <int D, int NP, bool SPLIT>
 __global__ void __launch_bounds__(kColWarps * 32, D == 64 ? 4 : 2)
 backward_columns_mma(Args a, int ntile) {
-  using SM = ColSmem<D, NP>;
+  using SM = ColSmem<D, NP, SPLIT>;
+  constexpr int kKeys = SM::kKeys;
   using SW = Swizzled<D>;
   constexpr int KS = D / 16, NT = D / 8;
   constexpr int kPieces = D * 2 / 16;
@@ -824,19 +828,20 @@ backward_columns_mma(Args a, int ntile) {
                                          kColWarps * 2 * SM::buffer);
   const int L = a.L, nq = a.nq, G = a.Hq / a.Hkv;
   const int seg = blockIdx.x / ntile;
-  const int j0 = (blockIdx.x % ntile) * 64;
+  const int j0 = (blockIdx.x % ntile) * kKeys;
   const int b = seg / a.Hkv, g = seg % a.Hkv;
-  const int kw = j0 + wid * 16;  // the warp's first key
+  const int kl = SPLIT ? 0 : wid * 16;  // the warp's first key in the tile
+  const int kw = j0 + kl;               // and in the cache
   const float sl2 = kLog2e / sqrtf((float)D), sc = 1.f / sqrtf((float)D);
 
   // K, V and the keys' spans
-  for (int e = threadIdx.x; e < 64 * kPieces; e += kColWarps * 32) {
+  for (int e = threadIdx.x; e < kKeys * kPieces; e += kColWarps * 32) {
     const int rr = e / kPieces, pc = e % kPieces;
     const int64_t at = ((int64_t)seg * L + min(j0 + rr, L - 1)) * D + pc * 8;
     cp_async16(sK + SW::at(rr, pc), reinterpret_cast<const bf*>(a.K) + at);
     cp_async16(sV + SW::at(rr, pc), reinterpret_cast<const bf*>(a.V) + at);
   }
-  if (threadIdx.x < 64) {
+  if (threadIdx.x < kKeys) {
     if (j0 + threadIdx.x < L)
       cp_async8(s_span + threadIdx.x,
                 a.span + (int64_t)seg * L + j0 + threadIdx.x);
@@ -851,7 +856,7 @@ backward_columns_mma(Args a, int ntile) {
   int hh = -1, blk = 0, last = -1;    // head of the group, block, last block
   int lbase = 0, low = 0x7FFFFFFF;    // window starts of chunks lbase + lane
   if (a.W_i && lane < chunks) low = a.lows[(int64_t)b * chunks + lane];
-  auto advance = [&]() {
+  auto advance_one = [&]() {
     if (kw >= L) return false;
     while (true) {
       while (++blk > last) {
@@ -872,6 +877,12 @@ backward_columns_mma(Args a, int ntile) {
       }
       if (__shfl_sync(kAll, low, c - lbase) <= jl) return true;
     }
+  };
+  int turn = 0;
+  auto advance = [&]() {
+    while (advance_one())
+      if (!SPLIT || (turn++ & (kColWarps - 1)) == wid) return true;
+    return false;
   };
   auto stage = [&](int buf) {
     unsigned char* dst = sB + buf * SM::buffer;
@@ -930,7 +941,7 @@ backward_columns_mma(Args a, int ntile) {
     if (any) {
       float x[2][4], dp[2][4];
       // places of the operands' pieces: rows of A are keys, of B query rows
-      const int ar = wid * 16 + (lane & 15), ap = lane >> 4;
+      const int ar = kl + (lane & 15), ap = lane >> 4;
       const int br = (lane & 7) + ((lane >> 4) << 3), bp = (lane >> 3) & 1;
       auto step = [&](float (&d)[2][4], const uint32_t (&A)[4],
                       const unsigned char* p, bool first) {
@@ -1001,6 +1012,33 @@ backward_columns_mma(Args a, int ntile) {
     __syncwarp();  // the buffer may be written again
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  if constexpr (SPLIT) {
+    // the other warps' sums through their buffers to the first warp
+    constexpr int kSum = 2 * D + 4;  // floats of a key, padded
+    static_assert(16 * kSum * 4 <= 2 * (int)SM::buffer, "sums fit");
+    auto each = [&](unsigned char* at, auto f) {
+      float* p = reinterpret_cast<float*>(at) + gr * kSum + 2 * tq;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          f(reinterpret_cast<float2*>(p + 8 * u * kSum + 8 * t), dk[t][2 * u],
+            dk[t][2 * u + 1]);
+          f(reinterpret_cast<float2*>(p + 8 * u * kSum + D + 8 * t),
+            dv[t][2 * u], dv[t][2 * u + 1]);
+        }
+    };
+    if (wid > 0)
+      each(sB, [](float2* p, float& x, float& y) { *p = make_float2(x, y); });
+    __syncthreads();
+    if (wid > 0) return;
+#pragma unroll 1
+    for (int w = 1; w < kColWarps; ++w)
+      each(sB + (size_t)w * 2 * SM::buffer, [](float2* p, float& x, float& y) {
+        x += p->x;
+        y += p->y;
+      });
+  }
   // The listed part.  A key's is the sum of rows [dK | dV]: one from its
   // first range (`top`), then the later ranges' shares (`carry`).  Up to
   // kShort rows are added by the lanes that hold the key, eight keys side by
@@ -1018,7 +1056,7 @@ backward_columns_mma(Args a, int ntile) {
   static_assert(16 * kRow * 4 <= 2 * (int)SM::buffer, "sums fit the buffers");
   constexpr int NV = 2 * D / 128;  // float4 per lane and row
   float* sums = reinterpret_cast<float*>(sB);
-  if (__any_sync(kAll, rows_of(s_span[wid * 16 + (lane & 15)]) > kShort)) {
+  if (__any_sync(kAll, rows_of(s_span[kl + (lane & 15)]) > kShort)) {
     const float* carry = a.carry + (int64_t)seg * a.w.ranges * 2 * D;
     const float* bsum = a.bsum + (int64_t)seg * a.w.blocks * 2 * D;
     const int64_t col = (int64_t)seg * L + kw;
@@ -1030,7 +1068,7 @@ backward_columns_mma(Args a, int ntile) {
       if (r > e) {  // the next long key
         do {
           if (++key >= 16) return nullptr;
-          sp = s_span[wid * 16 + key];
+          sp = s_span[kl + key];
         } while (rows_of(sp) <= kShort);
         r = sp.x / kRange;
         e = (sp.y - 1) / kRange;
@@ -1096,7 +1134,7 @@ backward_columns_mma(Args a, int ntile) {
     const int j = kw + gr + 8 * u;
     if (j >= L) continue;
     const int64_t col = (int64_t)seg * L + j;
-    const int2 sp = s_span[wid * 16 + gr + 8 * u];
+    const int2 sp = s_span[kl + gr + 8 * u];
     const int n = rows_of(sp), f = sp.x / kRange;
     auto add = [&](const float* p) {
 #pragma unroll
@@ -1144,16 +1182,30 @@ cudaError_t rows_as(const Args& a, cudaStream_t s) {
                 smem, s, a, ntile);
 }
 
-template <int D, int NP>
-cudaError_t columns_as(const Args& a, cudaStream_t s) {
-  const int ntile = (a.L + 63) / 64;
+template <int D, int NP, bool SPLIT>
+cudaError_t columns_run(const Args& a, cudaStream_t s) {
+  using SM = ColSmem<D, NP, SPLIT>;
+  const int ntile = (a.L + SM::kKeys - 1) / SM::kKeys;
   const int64_t ctas = (int64_t)a.w.segs * ntile;
   if (ctas > 0x7FFFFFFF) return cudaErrorNotSupported;
-  auto kern = backward_columns_mma<D, NP>;
-  cudaError_t e = ensure_smem(kern, ColSmem<D, NP>::bytes);
+  auto kern = backward_columns_mma<D, NP, SPLIT>;
+  cudaError_t e = ensure_smem(kern, SM::bytes);
   if (e != cudaSuccess) return e;
   return launch("backward_columns", kern, dim3((unsigned)ctas),
-                kColWarps * 32, ColSmem<D, NP>::bytes, s, a, ntile);
+                kColWarps * 32, SM::bytes, s, a, ntile);
+}
+
+template <int D, int NP>
+cudaError_t columns_as(const Args& a, cudaStream_t s) {
+  // Tiles of 64 keys that any window reaches.  Where they leave SMs without
+  // work, a CTA per 16 keys, its warps side by side on their rows (56 tiles
+  // with 4 heads of 100 rows, d = 64: 37 instead of 62 us; 128 tiles with 4
+  // heads of 160, d = 128: 117 instead of 158 us; 512 tiles with 2 heads: 236
+  // instead of 162 us).
+  const int64_t reach = a.W_i || a.W_h ? a.nq : (int64_t)a.nq + a.W;
+  const int64_t tiles = (min(reach, (int64_t)a.L) + 63) / 64 * a.w.segs;
+  return tiles <= sm_count() ? columns_run<D, NP, true>(a, s)
+                             : columns_run<D, NP, false>(a, s);
 }
 
 }  // namespace

@@ -115,6 +115,22 @@ def test_windows_and_sizes_of_each_head(dt):
     check(*x, idx, got)
 
 
+@pytest.mark.parametrize("dt,odt,d", [
+    (BF, BF, 64), (BF, BF, 128), (BF, F32, 64), (F32, F32, 64)])
+@pytest.mark.parametrize("per_query", [False, True])
+def test_many_heads(dt, odt, d, per_query):
+    """42 heads of keys: more tiles and entries than an SM's share, where
+    other tests have too few for all SMs; keys that every row selects."""
+    x = make(3, 260, 270, 28, 14, d, dt, odt, popular=3, scale=0.5)
+    W_i = None
+    if per_query:
+        g = torch.Generator(device="cuda").manual_seed(3)
+        W_i = torch.randint(1, 80, (3, 260), generator=g, device="cuda",
+                            dtype=torch.int32)
+    idx, _, got = run(*x, 40, 64, W_i=W_i)
+    check(*x, idx, got)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_peaked_scores(dt):
     """Scores up to the hundreds: probabilities of nearly one and of zero."""
@@ -333,12 +349,13 @@ def test_offsets_beyond_32_bits():
     assert not dK[0, -1][other].any() and not dV[0, -1][other].any()
 
 
-@pytest.mark.parametrize("dt,d,nq,W,k", [
-    (BF, 64, 700, 64, 32), (BF, 128, 300, 40, 64), (F32, 64, 300, 20, 16)])
-def test_debug_build(dt, d, nq, W, k):
+@pytest.mark.parametrize("dt,d,nq,W,k,heads", [
+    (BF, 64, 700, 64, 32, 2), (BF, 128, 300, 40, 64, 2),
+    (F32, 64, 300, 20, 16, 2), (BF, 64, 260, 40, 64, 42)])
+def test_debug_build(dt, d, nq, W, k, heads):
     """The index-checking build: no check fires, and equal bits."""
     from sparse_transformer_attention_b200 import binding, build
-    x = make(1, nq, nq, 4, 2, d, dt, dt, popular=8, scale=0.5)
+    x = make(1, nq, nq, 2 * heads, heads, d, dt, dt, popular=8, scale=0.5)
     idx, cnt, want = run(*x, W, k)
     prev = binding.use_library(build.build(debug=True))
     try:
