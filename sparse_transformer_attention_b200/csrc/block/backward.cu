@@ -302,7 +302,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) backward_rows(Args a) {
 // four, take 8 to 16 and left that pipe full (92% of its cycles) at 290 us in
 // the case of 6.5 M entries above; this takes 185 us, 9 TB/s from L2.  Plain
 // fp32 FMA keep the weights whole, too.  kRange = 128 was 213 us (fewer warps
-// with a longer tail), slots refilled one by one 192 us.
+// with a longer tail), 16 halves a small call (512 rows of 17: 12 -> 8 us) but
+// leaves four times the shares to the column pass (12 heads of 512 rows of 33:
+// 19 -> 13 us here, 17 -> 46 us there), slots refilled one by one 192 us.
 template <typename T, typename TD, int D>
 __global__ void __launch_bounds__(kListedWarps * 32)
 backward_listed(Args a, const uint32_t* keys, const uint32_t* ents) {
@@ -363,11 +365,11 @@ backward_listed(Args a, const uint32_t* keys, const uint32_t* ents) {
     }
     if (__all_sync(kAll, key[0] >= L)) return;  // sorted: none in use
   }
+  __syncwarp();  // `ent` is read by other lanes from here on
   const int64_t range = first + sub;
   uint32_t cur = range * kRange > 0 && range < a.w.ranges
                      ? (sub ? ent[sub * kRange - 1].x : keys[base + w0 - 1])
                      : 0xFFFFFFFFu;
-  __syncwarp();
   ent += sub * kRange;
   const int64_t at0 =
       (int64_t)seg * (a.Hq / a.Hkv) * a.nq * D + sl * EPL;
