@@ -5,7 +5,7 @@
 // places the entries (sort_place), which first orders its tile in shared
 // memory so that what it writes is runs of consecutive places: with entries
 // written where they stood, 32 lanes hit 32 sectors and placing 6.5 M entries
-// took 118 us where it takes 49.  Lists of one tile or a few (up to kSmall
+// took 118 us where it took 49.  Lists of one tile or a few (up to kSmall
 // entries) are sorted by one CTA each in shared memory, in one launch
 // instead of six (8704 entries: 18 us instead of 40).
 #include "../launch.cuh"
@@ -127,8 +127,30 @@ __device__ __forceinline__ uint32_t rank_step(uint32_t dg, bool in, int bits,
   return before + __popc(lower);
 }
 
+// The same with the lanes of each digit collected in shared memory, seen[]
+// (zero before and after), instead of by a vote per digit bit: 39 instead of
+// 47 us for 6.5 M entries.
+__device__ __forceinline__ uint32_t rank_seen(uint32_t dg, bool in,
+                                              uint32_t* seen, uint16_t* cnt) {
+  const int lane = threadIdx.x & 31;
+  if (in) atomicOr(seen + dg, 1u << lane);
+  __syncwarp();
+  const uint32_t same = seen[dg];
+  const uint32_t before = cnt[dg];
+  const uint32_t lower = same & ((1u << lane) - 1u);
+  __syncwarp();
+  if (in && lower == 0) {
+    cnt[dg] = (uint16_t)(before + __popc(same));
+    seen[dg] = 0;
+  }
+  __syncwarp();
+  return before + __popc(lower);
+}
+
 // Places a tile: the warps' runs are ranked, their counts chained, and the
-// tile, ordered by digit in shared memory, goes out run by run.
+// tile, ordered by digit in shared memory, goes out run by run.  Bound by
+// shared memory (79% of its cycles), two fifths of that bank conflicts of
+// scattered words; three CTAs per SM spill registers and take 44 us.
 __global__ void __launch_bounds__(kThreads, 2)
 sort_place(Args a, const uint32_t* key, const uint32_t* ent, uint32_t* key_out,
            uint32_t* ent_out, int shift, uint32_t mask) {
@@ -155,13 +177,17 @@ sort_place(Args a, const uint32_t* key, const uint32_t* ent, uint32_t* key_out,
   const size_t at_dg = (size_t)blockIdx.y * 256 + (mine ? dg : 0);
   const uint32_t all = mine ? a.totals[at_dg] : 0u;
   const uint32_t prior = a.hist[at_dg * a.w.tiles + blockIdx.x];
-  for (int c = threadIdx.x; c < kWarps * 256; c += kThreads)
+  // the digits' lanes lie in s_key, which is not needed before they are done
+  static_assert(kWarps * 256 <= kTile, "they fit");
+  for (int c = threadIdx.x; c < kWarps * 256; c += kThreads) {
     (&cnt[0][0])[c] = 0;
+    s_key[c] = 0;
+  }
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < kSteps; ++u)
-    rank[u] = rank_step((kv[u] >> shift) & mask, l0 + u * 32 + lane < n,
-                        a.w.digit, cnt[wid]);
+    rank[u] = rank_seen((kv[u] >> shift) & mask, l0 + u * 32 + lane < n,
+                        s_key + wid * 256, cnt[wid]);
   __syncthreads();
   {
     uint32_t total = 0;
