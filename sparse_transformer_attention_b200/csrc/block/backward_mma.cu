@@ -203,6 +203,29 @@ __device__ __forceinline__ void dot_operand(const unsigned char* row, int gr,
   }
 }
 
+// A block of 16 x 16 pairs of which some are masked.  Its products go through
+// the matrix instructions whole, where a masked pair's weight of zero does not
+// keep a NaN or infinity of a key (a row) from the other rows (keys).  Such a
+// value makes every score or dP of its row or key one, too, so the block's
+// sums of 0 x and 0 dP tell; then what is not finite is taken out of the last
+// products' operands, and the pairs that do attend to it carry NaN weights.
+__device__ __forceinline__ bool not_finite(const float (&x)[2][4],
+                                           const float (&dp)[2][4]) {
+  float z = 0.f;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) z = fmaf(x[t][c], 0.f, fmaf(dp[t][c], 0.f, z));
+  return __any_sync(kAll, z != 0.f);
+}
+__device__ __forceinline__ void finite_only(uint32_t (&f)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if ((f[c] & 0x7F80u) == 0x7F80u) f[c] &= 0xFFFF0000u;
+    if ((f[c] & 0x7F800000u) == 0x7F800000u) f[c] &= 0xFFFFu;
+  }
+}
+
 // The largest of the warp's values.
 __device__ __forceinline__ float warp_max(float x) {
   float r;
@@ -366,8 +389,9 @@ backward_rows_mma(Args a, int ntile) {
         for (int ks = 0; ks < KS; ++ks) operand(p, ks, held[p][ks]);
   };
   hold();
-  // scores (log2 units, masked to -inf) and dP of the 16 x 16 block of keys
-  // kb.. (at place kl of the staged chunk), as two accumulators of 8 keys
+  // scores (log2 units, masked to -inf) and dP (masked to 0) of the 16 x 16
+  // block of keys kb.. (at place kl of the staged chunk), as two accumulators
+  // of 8 keys; true where a masked block holds what is not finite
   auto block = [&](const unsigned char* sk, int stride, int kb, bool anchor,
                    float (&x)[2][4], float (&dp)[2][4]) {
     const unsigned char* at = sk + ((lane & 7) + ((lane >> 4) << 3)) * RS +
@@ -404,8 +428,9 @@ backward_rows_mma(Args a, int ntile) {
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[t][c] *= sl2;
-      return;
+      return false;
     }
+    const bool bad = not_finite(x, dp);
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -415,7 +440,9 @@ backward_rows_mma(Args a, int ntile) {
             ? va && (anchor ? j == 0 && loa > 0 : j >= loa && j <= ia)
             : vb && (anchor ? j == 0 && lob > 0 : j >= lob && j <= ib);
         x[t][c] = ok ? x[t][c] * sl2 : -INFINITY;
+        dp[t][c] = ok ? dp[t][c] : 0.f;
       }
+    return bad;
   };
   // this warp's first block of keys in the chunk that begins at cs
   auto first_block = [&](int cs) {
@@ -684,7 +711,7 @@ backward_rows_mma(Args a, int ntile) {
     const float Di[2] = {s_D[sr], s_D[sr + 8]};
     auto add = [&](const unsigned char* sk, int stride, int kb, bool anchor) {
       float x[2][4], dp[2][4];
-      block(sk, stride, kb, anchor, x, dp);
+      const bool bad = block(sk, stride, kb, anchor, x, dp);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -706,6 +733,7 @@ backward_rows_mma(Args a, int ntile) {
       for (int t = 0; t < NT; t += 2) {
         uint32_t f[4];
         ldsm4t(f, kp + t * 16);
+        if (bad) finite_only(f);
         mma(o[t], hi[0], hi[1], hi[2], hi[3], f[0], f[1]);
         mma(o[t], lo[0], lo[1], lo[2], lo[3], f[0], f[1]);
         mma(o[t + 1], hi[0], hi[1], hi[2], hi[3], f[2], f[3]);
@@ -807,6 +835,31 @@ __device__ __forceinline__ void cp_async8(void* dst, const void* src) {
                    (uint32_t)__cvta_generic_to_shared(dst)),
                "l"(src)
                : "memory");
+}
+
+// Takes out what is not finite of a warp's 16 rows of q and dO; a row whose dO
+// was not gets such a log-sum-exp.  (Out of line: inlined, its registers made
+// the kernel spill.)
+template <int D, int NP>
+__device__ __noinline__ void finite_rows(unsigned char* own) {
+  constexpr int kPieces = D * 2 / 16, kRows = 16 * D * 2;
+  const int lane = threadIdx.x & 31;
+  bool mine = false;
+#pragma unroll 1
+  for (int e = lane >> 4; e < (1 + NP) * kPieces; e += 2) {
+    const int p = e / kPieces;
+    uint4* v = reinterpret_cast<uint4*>(
+        own + p * kRows + Swizzled<D>::at(lane & 15, e % kPieces));
+    uint32_t f[4] = {v->x, v->y, v->z, v->w};
+    finite_only(f);
+    if (p > 0)
+      mine |= f[0] != v->x || f[1] != v->y || f[2] != v->z || f[3] != v->w;
+    *v = make_uint4(f[0], f[1], f[2], f[3]);
+  }
+  mine |= __shfl_xor_sync(kAll, mine, 16);
+  if (mine && lane < 16)
+    reinterpret_cast<float2*>(own + (1 + NP) * kRows)[lane].x = NAN;
+  __syncwarp();
 }
 
 template <int D, int NP, bool SPLIT>
@@ -963,6 +1016,9 @@ backward_columns_mma(Args a, int ntile) {
           step(dp, A, sG + p * SM::rows + SW::at(br, 2 * ks + bp),
                ks == 0 && p == 0);
       }
+      if (!inner && not_finite(x, dp)) {
+        finite_rows<D, NP>(sB + buf * SM::buffer);
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -977,7 +1033,8 @@ backward_columns_mma(Args a, int ntile) {
             const float p =
                 ok ? ex2(fmaf(x[t][c + 2 * u], sl2, -st.x)) : 0.f;
             x[t][c + 2 * u] = p;
-            dp[t][c + 2 * u] = p * (dp[t][c + 2 * u] - st.y) * sc;
+            dp[t][c + 2 * u] =
+                ok ? p * (dp[t][c + 2 * u] - st.y) * sc : 0.f;
           }
         }
       uint32_t ph[4], pl[4], dh[4], dl[4];
@@ -1000,7 +1057,7 @@ backward_columns_mma(Args a, int ntile) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           ldsm4t(f, sG + p * SM::rows + SW::at(tr, t + tp));
-          mma(dv[t], ph[0], ph[1], ph[2], ph[3], f[0], f[1]);
+            mma(dv[t], ph[0], ph[1], ph[2], ph[3], f[0], f[1]);
           mma(dv[t + 1], ph[0], ph[1], ph[2], ph[3], f[2], f[3]);
           if (p == 0) {  // lo x lo is below what two parts keep
             mma(dv[t], pl[0], pl[1], pl[2], pl[3], f[0], f[1]);

@@ -367,6 +367,64 @@ def test_debug_build(dt, d, nq, W, k, heads):
     assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+@pytest.mark.parametrize("dt,odt,d", [
+    (BF, BF, 64), (BF, F32, 64), (BF, BF, 128), (F32, F32, 64)])
+@pytest.mark.parametrize("nq,L,heads", [(200, 777, 1), (300, 300, 1),
+                                        (260, 270, 42)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_not_finite_where_others_attend(dt, odt, d, nq, L, heads, value):
+    """A key (a row) that is not finite reaches the gradients of the rows that
+    attend to it (the keys that it attends to) and no others: those keep their
+    bits, next to it in the same tile as anywhere."""
+    W, k = 40, 16
+    Q, K, V, dO = make(1, nq, L, 2 * heads, heads, d, dt, odt)
+    idx, cnt, base = run(Q, K, V, dO, W, k)
+
+    def grads(q, kk, v, g):
+        return ca.condensate_attn_prefill_backward(q, kk, v, g, idx, cnt, W, k)
+
+    def same(x, y, attended, what):
+        assert torch.equal(x[~attended], y[~attended]), what
+        assert not torch.isfinite(x[attended]).all(-1).any(), what
+
+    p0 = L - nq
+    for j in (1, p0 + 100, p0 + 104, L - 2):
+        attended = (idx == j).any(-1)  # [1, Hq, nq]
+        attended[:, 2:] = False        # the other kv heads' keys stay
+        for n in (1, 2):
+            x = [Q, K, V, dO]
+            x[n] = x[n].clone()
+            x[n][0, 0, j] = value
+            got = grads(*x)
+            # dQ of another row of the head may only stay; rows that attend
+            # to an infinite key with a score of -inf may stay, too
+            if n == 1 and value == float("inf"):
+                assert torch.equal(got[0][~attended], base[0][~attended]), j
+            else:
+                same(got[0], base[0], attended, ("dQ", n, j))
+    for i in (0, 100, nq - 1):
+        keys = torch.zeros(L + 1, dtype=torch.bool, device="cuda")
+        at = idx[0, 0, i].long()
+        keys[torch.where(at < 0, L, at)] = True
+        attended = torch.zeros(1, heads, L, dtype=torch.bool, device="cuda")
+        attended[0, 0] = keys[:L]
+        for n in (0, 3):
+            x = [Q, K, V, dO]
+            x[n] = x[n].clone()
+            x[n][0, 0, i] = value
+            got = grads(*x)
+            rows = torch.ones(2 * heads, nq, dtype=torch.bool, device="cuda")
+            rows[0, i] = False
+            assert torch.equal(got[0][0][rows], base[0][0][rows]), (n, i)
+            for y in (1, 2):
+                assert torch.equal(got[y][~attended], base[y][~attended]), \
+                    (n, i, y)
+            if n == 3:
+                same(got[2], base[2], attended, ("dV", n, i))
+            if value != value:
+                same(got[1], base[1], attended, ("dK", n, i))
+
+
 def test_refusals():
     Q, K, V, dO = make(1, 64, 64, 2, 1, 64, BF, BF)
     _, idx, cnt = ca.condensate_attn_prefill(Q, K, V, 16, 4)
