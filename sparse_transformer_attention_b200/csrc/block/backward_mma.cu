@@ -821,7 +821,7 @@ struct ColSmem {
   // of a warp: two buffers of q, the planes of dO, (log-sum-exp, D), windows
   static constexpr size_t buffer = (1 + NP) * rows + 16 * 12;
   static constexpr size_t bytes =
-      2 * keys + kColWarps * 2 * buffer + kKeys * sizeof(int2);
+      2 * keys + kColWarps * 2 * buffer + 64 * sizeof(int2);
 };
 
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
@@ -864,7 +864,7 @@ __device__ __noinline__ void finite_rows(unsigned char* own) {
 
 template <int D, int NP, bool SPLIT>
 __global__ void __launch_bounds__(kColWarps * 32, D == 64 ? 4 : 2)
-backward_columns_mma(Args a, int ntile) {
+backward_columns_mma(Args a, int ntile, int first) {
   using SM = ColSmem<D, NP, SPLIT>;
   constexpr int kKeys = SM::kKeys;
   using SW = Swizzled<D>;
@@ -880,21 +880,34 @@ backward_columns_mma(Args a, int ntile) {
   int2* s_span = reinterpret_cast<int2*>(sV + SM::keys +
                                          kColWarps * 2 * SM::buffer);
   const int L = a.L, nq = a.nq, G = a.Hq / a.Hkv;
-  const int seg = blockIdx.x / ntile;
-  const int j0 = (blockIdx.x % ntile) * kKeys;
+  // Behind the tiles that windows reach, from key `first` on, come those of
+  // 64 earlier keys, which have a listed part only.
+  const int rest = (int)blockIdx.x - a.w.segs * ntile;
+  bool early = rest >= 0;
+  const int seg = early ? rest / (first / 64) : blockIdx.x / ntile;
+  const int j0 = early ? rest % (first / 64) * 64
+                       : first + (blockIdx.x % ntile) * kKeys;
+  const int count = early ? 64 : kKeys;
   const int b = seg / a.Hkv, g = seg % a.Hkv;
-  const int kl = SPLIT ? 0 : wid * 16;  // the warp's first key in the tile
+  const int kl = SPLIT && !early ? 0 : wid * 16;  // the warp's first key in
+                                                  // the tile
   const int kw = j0 + kl;               // and in the cache
   const float sl2 = kLog2e / sqrtf((float)D), sc = 1.f / sqrtf((float)D);
+  if (!SPLIT && (a.W_i || a.W_h) && j0 + 64 <= a.p0) {  // early after all?
+    int wm = a.W_i ? a.wmax[b] : 1;
+    for (int u = 0; a.W_h && u < G; ++u) wm = max(wm, a.W_h[g * G + u]);
+    early = (int64_t)j0 + 63 + wm - 1 < a.p0;
+  }
 
   // K, V and the keys' spans
-  for (int e = threadIdx.x; e < kKeys * kPieces; e += kColWarps * 32) {
+  for (int e = threadIdx.x; !early && e < kKeys * kPieces;
+       e += kColWarps * 32) {
     const int rr = e / kPieces, pc = e % kPieces;
     const int64_t at = ((int64_t)seg * L + min(j0 + rr, L - 1)) * D + pc * 8;
     cp_async16(sK + SW::at(rr, pc), reinterpret_cast<const bf*>(a.K) + at);
     cp_async16(sV + SW::at(rr, pc), reinterpret_cast<const bf*>(a.V) + at);
   }
-  if (threadIdx.x < kKeys) {
+  if (threadIdx.x < count) {
     if (j0 + threadIdx.x < L)
       cp_async8(s_span + threadIdx.x,
                 a.span + (int64_t)seg * L + j0 + threadIdx.x);
@@ -910,7 +923,7 @@ backward_columns_mma(Args a, int ntile) {
   int lbase = 0, low = 0x7FFFFFFF;    // window starts of chunks lbase + lane
   if (a.W_i && lane < chunks) low = a.lows[(int64_t)b * chunks + lane];
   auto advance_one = [&]() {
-    if (kw >= L) return false;
+    if (early || kw >= L) return false;
     while (true) {
       while (++blk > last) {
         if (++hh >= G) return false;
@@ -1069,7 +1082,7 @@ backward_columns_mma(Args a, int ntile) {
     __syncwarp();  // the buffer may be written again
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  if constexpr (SPLIT) {
+  if (SPLIT && !early) {
     // the other warps' sums through their buffers to the first warp
     constexpr int kSum = 2 * D + 4;  // floats of a key, padded
     static_assert(16 * kSum * 4 <= 2 * (int)SM::buffer, "sums fit");
@@ -1105,6 +1118,20 @@ backward_columns_mma(Args a, int ntile) {
   // their sum, and leaves each key's total in shared memory (its row buffers
   // are free now).
   __syncwarp();
+  {
+    const int2 sp = s_span[kl + (lane & 15)];
+    if (early && !__any_sync(kAll, sp.y > sp.x)) {  // 16 keys nobody lists
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      const int64_t at = ((int64_t)seg * L + kw) * D;
+      uint4* ok = reinterpret_cast<uint4*>(reinterpret_cast<bf*>(a.dK) + at);
+      uint4* ov = reinterpret_cast<uint4*>(reinterpret_cast<bf*>(a.dV) + at);
+#pragma unroll
+      for (int u = 0; u < D / 16; ++u) ok[32 * u + lane] = zero;
+#pragma unroll
+      for (int u = 0; u < D / 16; ++u) ov[32 * u + lane] = zero;
+      return;
+    }
+  }
   constexpr int kShort = 4;
   auto rows_of = [&](const int2& sp) {
     return sp.y > sp.x ? (sp.y - 1) / kRange - sp.x / kRange + 1 : 0;
@@ -1240,29 +1267,32 @@ cudaError_t rows_as(const Args& a, cudaStream_t s) {
 }
 
 template <int D, int NP, bool SPLIT>
-cudaError_t columns_run(const Args& a, cudaStream_t s) {
+cudaError_t columns_run(const Args& a, int first, cudaStream_t s) {
   using SM = ColSmem<D, NP, SPLIT>;
-  const int ntile = (a.L + SM::kKeys - 1) / SM::kKeys;
-  const int64_t ctas = (int64_t)a.w.segs * ntile;
+  const int ntile = (a.L - first + SM::kKeys - 1) / SM::kKeys;
+  const int64_t ctas = (int64_t)a.w.segs * (ntile + first / 64);
   if (ctas > 0x7FFFFFFF) return cudaErrorNotSupported;
   auto kern = backward_columns_mma<D, NP, SPLIT>;
   cudaError_t e = ensure_smem(kern, SM::bytes);
   if (e != cudaSuccess) return e;
   return launch("backward_columns", kern, dim3((unsigned)ctas),
-                kColWarps * 32, SM::bytes, s, a, ntile);
+                kColWarps * 32, SM::bytes, s, a, ntile, first);
 }
 
 template <int D, int NP>
 cudaError_t columns_as(const Args& a, cudaStream_t s) {
-  // Tiles of 64 keys that any window reaches.  Where they leave SMs without
-  // work, a CTA per 16 keys, its warps side by side on their rows (56 tiles
-  // with 4 heads of 100 rows, d = 64: 37 instead of 62 us; 128 tiles with 4
-  // heads of 160, d = 128: 117 instead of 158 us; 512 tiles with 2 heads: 236
-  // instead of 162 us).
-  const int64_t reach = a.W_i || a.W_h ? a.nq : (int64_t)a.nq + a.W;
-  const int64_t tiles = (min(reach, (int64_t)a.L) + 63) / 64 * a.w.segs;
-  return tiles <= sm_count() ? columns_run<D, NP, true>(a, s)
-                             : columns_run<D, NP, false>(a, s);
+  // The keys before any window (windows on the device may reach all): a chunk
+  // of 777 rows behind 130000 keys, 4 heads of d = 64, 85 us, as window tiles
+  // 146 us; 64 rows behind 600000, 171 instead of 302 us.
+  const int first =
+      a.W_i || a.W_h ? 0 : (int)max((int64_t)a.p0 - a.W + 1, (int64_t)0) & ~63;
+  // Where the other keys, in tiles of 64, leave SMs without work, a CTA per 16
+  // keys, its warps side by side on their rows (56 tiles with 4 heads of 100
+  // rows, d = 64: 37 instead of 62 us; 128 tiles with 4 heads of 160, d = 128:
+  // 117 instead of 158 us; 512 tiles with 2 heads: 236 instead of 162 us).
+  const int64_t tiles = ((int64_t)a.L - first + 63) / 64 * a.w.segs;
+  return tiles <= sm_count() ? columns_run<D, NP, true>(a, first, s)
+                             : columns_run<D, NP, false>(a, first, s);
 }
 
 }  // namespace

@@ -117,11 +117,13 @@ def test_windows_and_sizes_of_each_head(dt):
 
 @pytest.mark.parametrize("dt,odt,d", [
     (BF, BF, 64), (BF, BF, 128), (BF, F32, 64), (F32, F32, 64)])
-@pytest.mark.parametrize("per_query", [False, True])
-def test_many_heads(dt, odt, d, per_query):
+@pytest.mark.parametrize("L,per_query", [(270, False), (270, True),
+                                         (1100, False), (1100, True)])
+def test_many_heads(dt, odt, d, L, per_query):
     """42 heads of keys: more tiles and entries than an SM's share, where
-    other tests have too few for all SMs; keys that every row selects."""
-    x = make(3, 260, 270, 28, 14, d, dt, odt, popular=3, scale=0.5)
+    other tests have too few for all SMs; keys that every row selects; keys
+    before any window."""
+    x = make(3, 260, L, 28, 14, d, dt, odt, popular=3, scale=0.5)
     W_i = None
     if per_query:
         g = torch.Generator(device="cuda").manual_seed(3)
