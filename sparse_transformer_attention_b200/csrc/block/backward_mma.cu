@@ -84,7 +84,7 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t* hi,
 }
 
 // ---------------------------------------------------------------- row pass
-// A CTA owns 64 query rows of one head, a warp 16.  In order:
+// A CTA owns 64 query rows of one head (16 in small calls).  In order:
 //   1. the window's and the anchor's scores and dP: running (max, sum e,
 //      sum e dP) of each row;
 //   2. row by row, the Top-k, 16 gathered K and V rows at a time: as A
@@ -113,25 +113,27 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t* hi,
 // 64 to 256 + 64 keys, d = 128: 386 us.  Three CTAs of 80 registers per SM
 // instead of two of 128 were slower (352 us at d = 64).
 constexpr int kRowWarps = 8;
-constexpr int kWarpRows = 64 / kRowWarps;  // Top-k rows of a warp
 
-template <int D, int NP>
+template <int D, int NP, int ROWS>
 struct RowSmem {
+  static constexpr int kGroups = ROWS / 16;            // of 16 rows
+  static constexpr int kShare = kRowWarps / kGroups;   // warps of a group
+  static constexpr int kWarpRows = ROWS / kRowWarps;   // Top-k rows of a warp
   static constexpr int CK = D == 64 ? 64 : 32;  // keys of a chunk
   static constexpr int RS = D * 2 + 16; // padded row (bytes)
-  static constexpr size_t rows = (size_t)(NP + 1) * 64 * RS;   // q, dO
+  static constexpr size_t rows = (size_t)(NP + 1) * ROWS * RS;   // q, dO
   static constexpr size_t chunk = (size_t)2 * CK * RS;         // K, V
   static constexpr size_t anchor = (size_t)2 * 16 * RS;        // K, V
   // dQ's window part, in the chunks' place at the end: rows of DS floats, no
   // two of 8 rows on a bank
   static constexpr int DS = D + 8;
-  static_assert((size_t)64 * DS * 4 <= 2 * chunk, "dQ fits the chunks");
-  static constexpr size_t stat = (size_t)64 * 4;  // one number per row
+  static_assert((size_t)ROWS * DS * 4 <= 2 * chunk, "dQ fits the chunks");
+  static constexpr size_t stat = (size_t)ROWS * 4;  // one number per row
   __host__ __device__ static size_t bytes(int k) {
     const size_t kk = (k + 15) / 16 * 16;
-    // 2 x 3 running sums, the log-sum-exp, D, the Top-k count
-    return rows + 2 * chunk + anchor + 9 * stat +
-           kRowWarps * kk * 8 + 64 * kk * 4;
+    // each warp's 3 running sums, the log-sum-exp, D, the Top-k count
+    return rows + 2 * chunk + anchor + (3 * kShare + 3) * stat +
+           kRowWarps * kk * 8 + ROWS * kk * 4;
   }
 };
 
@@ -233,11 +235,13 @@ __device__ __forceinline__ float warp_max(float x) {
   return r;
 }
 
-template <int D, int NP>
+template <int D, int NP, int ROWS>
 __global__ void __launch_bounds__(kRowWarps * 32, 2)
 backward_rows_mma(Args a, int ntile) {
-  using SM = RowSmem<D, NP>;
+  using SM = RowSmem<D, NP, ROWS>;
   constexpr int RS = SM::RS, CK = SM::CK, DS = SM::DS;
+  constexpr int kGroups = SM::kGroups, kShare = SM::kShare;
+  constexpr int kWarpRows = SM::kWarpRows;
   constexpr int KS = D / 16;  // steps of a product over the head dimension
   constexpr int NT = D / 8;   // its 8-wide tiles
   // q's and dO's operands of the window products: in registers where they
@@ -247,11 +251,12 @@ backward_rows_mma(Args a, int ntile) {
   chain();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int gr = lane >> 2, tq = lane & 3;
-  const int rg = wid & 3, hf = wid >> 2;  // row group, which half of its work
+  const int rg = wid % kGroups, hf = wid / kGroups;  // row group, which share
+                                                     // of its work
   const int k = a.k, kk = (k + 15) / 16 * 16;
   const int nq = a.nq, L = a.L;
   const int bh = blockIdx.x / ntile;
-  const int r0 = (blockIdx.x % ntile) * 64;
+  const int r0 = (blockIdx.x % ntile) * ROWS;
   const int b = bh / a.Hq, h = bh % a.Hq;
   const int seg = b * a.Hkv + h / (a.Hq / a.Hkv);
   const int64_t rowbase = (int64_t)bh * nq;
@@ -261,28 +266,28 @@ backward_rows_mma(Args a, int ntile) {
   unsigned char* sR = g_smem;              // q and dO
   unsigned char* sC = sR + SM::rows;       // two chunks of K and V
   unsigned char* sA = sC + 2 * SM::chunk;  // the first 16 keys
-  float* s_part = reinterpret_cast<float*>(sA + SM::anchor);  // [half][m, l,
-                                                              //  E][row]
-  float* s_lse = s_part + 6 * 64;
-  float* s_D = s_lse + 64;
-  int* s_top = reinterpret_cast<int*>(s_D + 64);  // Top-k entries of a row
-  float2* s_xd = reinterpret_cast<float2*>(s_top + 64) + wid * kk;
+  float* s_part = reinterpret_cast<float*>(sA + SM::anchor);  // [share][m,
+                                                              //  l, E][row]
+  float* s_lse = s_part + 3 * kShare * ROWS;
+  float* s_D = s_lse + ROWS;
+  int* s_top = reinterpret_cast<int*>(s_D + ROWS);  // Top-k entries of a row
+  float2* s_xd = reinterpret_cast<float2*>(s_top + ROWS) + wid * kk;
   int* s_idx = reinterpret_cast<int*>(
-      reinterpret_cast<float2*>(s_top + 64) + kRowWarps * kk);
+      reinterpret_cast<float2*>(s_top + ROWS) + kRowWarps * kk);
   const float sl2 = kLog2e / sqrtf((float)D), sc = 1.f / sqrtf((float)D);
   constexpr int kPieces = D * 2 / 16;  // 16-byte pieces of a row
 
-  // the keys that the CTA's rows see: every warp looks at all 64 rows
+  // the keys that the CTA's rows see: every warp looks at all rows
   int kmin_c = 0x7FFFFFFF;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < (ROWS + 31) / 32; ++u) {
     int w;
-    kmin_c = min(kmin_c, window_lo(a, b, h, min(r0 + 32 * u + lane, nq - 1),
+    kmin_c = min(kmin_c, window_lo(a, b, h, min(r0 + 32 * u + lane % ROWS, nq - 1),
                                    false, &w));
   }
   kmin_c = __reduce_min_sync(kAll, kmin_c);
   const int cs0 = kmin_c & ~15;
-  const int kmax_c = a.p0 + min(r0 + 63, nq - 1);
+  const int kmax_c = a.p0 + min(r0 + ROWS - 1, nq - 1);
   const int nch = (kmax_c - cs0) / CK + 1;
   auto copy_keys = [&](unsigned char* dst, int first, int count, int stride) {
     for (int e = threadIdx.x; e < count * kPieces; e += kRowWarps * 32) {
@@ -299,14 +304,14 @@ backward_rows_mma(Args a, int ntile) {
                 min(CK, (kmax_c + 1 - cs0 - ch * CK + 15) & ~15), CK);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  for (int e = threadIdx.x; e < 64 * kPieces; e += kRowWarps * 32) {
+  for (int e = threadIdx.x; e < ROWS * kPieces; e += kRowWarps * 32) {
     const int rr = e / kPieces, pc = e % kPieces;
     const int64_t at = (int64_t)min(r0 + rr, nq - 1) * D + pc * 8;
     unsigned char* dst = sR + rr * RS + pc * 16;
     cp_async16(dst, Qg + at);
 #pragma unroll
     for (int p = 0; p < NP; ++p)
-      cp_async16(dst + (size_t)(p + 1) * 64 * RS, a.g[p] + rowbase * D + at);
+      cp_async16(dst + (size_t)(p + 1) * ROWS * RS, a.g[p] + rowbase * D + at);
   }
   copy_keys(sA, 0, 16, 16);
   stage(0);
@@ -377,7 +382,7 @@ backward_rows_mma(Args a, int ntile) {
   __syncthreads();
   // A operands of the window products: q (plane 0) and dO of the warp's rows
   auto operand = [&](int plane, int ks, uint32_t (&A)[4]) {
-    ldsm4(A, sR + (size_t)plane * 64 * RS +
+    ldsm4(A, sR + (size_t)plane * ROWS * RS +
                  (rg * 16 + (lane & 15)) * RS + (lane >> 4) * 16 + ks * 32);
   };
   uint32_t held[kHold ? 2 : 1][kHold ? KS : 1][4];
@@ -444,10 +449,11 @@ backward_rows_mma(Args a, int ntile) {
       }
     return bad;
   };
-  // this warp's first block of keys in the chunk that begins at cs
+  // this warp's first block of keys in the chunk that begins at cs, of every
+  // kShare-th one
   auto first_block = [&](int cs) {
     const int kb = max(cs, kmin & ~15);
-    return kb + (((kb >> 4) ^ hf) & 1) * 16;
+    return kb + ((hf - (kb >> 4)) & (kShare - 1)) * 16;
   };
 
   // ---- 1: window and anchor, running sums
@@ -490,7 +496,7 @@ backward_rows_mma(Args a, int ntile) {
       const int cs = cs0 + ch * CK;
 #pragma unroll 1
       for (int kb = first_block(cs); wlive && kb <= min(cs + CK - 1, kmax);
-           kb += 32) {
+           kb += 16 * kShare) {
         float x[2][4], dp[2][4];
         block(sC + (ch & 1) * SM::chunk + (kb - cs) * RS, CK, kb, false, x, dp);
         add(x, dp);
@@ -508,10 +514,10 @@ backward_rows_mma(Args a, int ntile) {
       ll += __shfl_xor_sync(kAll, ll, 2);
       EE += __shfl_xor_sync(kAll, EE, 2);
       if (tq == 0) {
-        float* p = s_part + hf * 3 * 64 + rg * 16 + gr + 8 * u;
+        float* p = s_part + hf * 3 * ROWS + rg * 16 + gr + 8 * u;
         p[0] = mx;
-        p[64] = ll;
-        p[128] = EE;
+        p[ROWS] = ll;
+        p[2 * ROWS] = EE;
       }
     }
     __syncthreads();
@@ -530,15 +536,19 @@ backward_rows_mma(Args a, int ntile) {
     const uint32_t sel0 = gr >= 4 ? 0x1044u : 0x4410u;
     const uint32_t sel1 = gr >= 4 ? 0x3244u : 0x4432u;
     const uint32_t ones = 0x3F803F80u;  // two bf16 ones
-    // the running sums of both warps of a pair, a row per lane
+    // the running sums of a group's warps together, a row per lane
     float pm = 0.f, pl = 0.f, pE = 0.f;
     if (lane < nrow) {
       const float* p = s_part + t_row + lane;
-      const float m1 = p[0], m2 = p[3 * 64];
-      pm = fmaxf(m1, m2);
-      const float f1 = ex2(m1 - pm), f2 = ex2(m2 - pm);
-      pl = p[64] * f1 + p[4 * 64] * f2;
-      pE = p[128] * f1 + p[5 * 64] * f2;
+      pm = p[0];
+#pragma unroll
+      for (int u = 1; u < kShare; ++u) pm = fmaxf(pm, p[3 * u * ROWS]);
+#pragma unroll
+      for (int u = 0; u < kShare; ++u) {
+        const float f = ex2(p[3 * u * ROWS] - pm);
+        pl = fmaf(p[(3 * u + 1) * ROWS], f, pl);
+        pE = fmaf(p[(3 * u + 2) * ROWS], f, pE);
+      }
     }
     Gather<D> kr, vr;
     int j[4];  // the entries in kr and vr (-1: none, row 0 is read)
@@ -564,7 +574,7 @@ backward_rows_mma(Args a, int ntile) {
       dot_operand<NL>(sR + tr * RS, gr, tq, wq);
 #pragma unroll
       for (int p = 0; p < NP; ++p)
-        dot_operand<NL>(sR + (size_t)(p + 1) * 64 * RS + tr * RS, gr, tq,
+        dot_operand<NL>(sR + (size_t)(p + 1) * ROWS * RS + tr * RS, gr, tq,
                         wg[p]);
       // sums: acc of the rows' dimensions, sum of the weights alone (columns
       // 0, 1: e dP, columns 2, 3: e)
@@ -687,7 +697,7 @@ backward_rows_mma(Args a, int ntile) {
 
   // ---- 3: dS of the window and the anchor
   __syncthreads();
-  float o[NT][4];  // of the pair's first warp with the listed part
+  float o[NT][4];  // of the group's first warp with the listed part
   {
     const float* pa = a.dql + (rowbase + ca) * D + 2 * tq;
     const float* pb = a.dql + (rowbase + cb) * D + 2 * tq;
@@ -752,15 +762,15 @@ backward_rows_mma(Args a, int ntile) {
       const int cs = cs0 + ch * CK;
 #pragma unroll 1
       for (int kb = first_block(cs); wlive && kb <= min(cs + CK - 1, kmax);
-           kb += 32)
+           kb += 16 * kShare)
         add(sC + (ch & 1) * SM::chunk + (kb - cs) * RS, CK, kb, false);
     }
   }
-  // dQ: the pair's first warp's part, then the second's
+  // dQ: the parts of a group's warps, one after the other
   __syncthreads();
   float* s_dq = reinterpret_cast<float*>(sC);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
+#pragma unroll 1
+  for (int u = 0; u < kShare; ++u) {
     if (u == hf) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -768,7 +778,7 @@ backward_rows_mma(Args a, int ntile) {
             s_dq + (rg * 16 + gr) * DS + 8 * t + 2 * tq);
         float2* pb = pa + 4 * DS;
         float2 x = make_float2(0.f, 0.f), y = x;
-        if (u == 1) {
+        if (u > 0) {
           x = *pa;
           y = *pb;
         }
@@ -779,7 +789,7 @@ backward_rows_mma(Args a, int ntile) {
     __syncthreads();
   }
   bf* dQ = reinterpret_cast<bf*>(a.dQ) + (rowbase + r0) * D;
-  const int live = min(64, nq - r0);
+  const int live = min(ROWS, nq - r0);
   for (int e = threadIdx.x; e < live * (D / 8); e += kRowWarps * 32)
     reinterpret_cast<uint4*>(dQ)[e] =
         pack16<bf>(s_dq + e / (D / 8) * DS + e % (D / 8) * 8);
@@ -1253,17 +1263,29 @@ backward_columns_mma(Args a, int ntile, int first) {
 }
 
 // --------------------------------------------------------------- host side
-template <int D, int NP>
-cudaError_t rows_as(const Args& a, cudaStream_t s) {
-  const int ntile = (a.nq + 63) / 64;
+template <int D, int NP, int ROWS>
+cudaError_t rows_run(const Args& a, cudaStream_t s) {
+  const int ntile = (a.nq + ROWS - 1) / ROWS;
   const int64_t ctas = (int64_t)a.B * a.Hq * ntile;
   if (ctas > 0x7FFFFFFF) return cudaErrorNotSupported;
-  const size_t smem = RowSmem<D, NP>::bytes(a.k);
-  auto kern = backward_rows_mma<D, NP>;
+  const size_t smem = RowSmem<D, NP, ROWS>::bytes(a.k);
+  auto kern = backward_rows_mma<D, NP, ROWS>;
   cudaError_t e = ensure_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch("backward_rows", kern, dim3((unsigned)ctas), kRowWarps * 32,
                 smem, s, a, ntile);
+}
+
+template <int D, int NP>
+cudaError_t rows_as(const Args& a, cudaStream_t s) {
+  // 16 rows to a CTA while all of those are resident at once, two per SM: a
+  // warp's chain of Top-k rows is then 2 instead of 8 (26 CTAs of 64 rows of
+  // 64 to 256 + 64 keys, d = 128: 37 instead of 78 us; 24 of 64 + 32 keys,
+  // d = 64: 15 instead of 25 us; with 96 of these it would be 27 instead of
+  // 25 us, with 384 72 instead of 57 us).
+  const int64_t few = (int64_t)a.B * a.Hq * ((a.nq + 15) / 16);
+  return few <= 2 * (int64_t)sm_count() ? rows_run<D, NP, 16>(a, s)
+                                        : rows_run<D, NP, 64>(a, s);
 }
 
 template <int D, int NP, bool SPLIT>

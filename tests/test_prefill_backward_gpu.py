@@ -116,7 +116,8 @@ def test_windows_and_sizes_of_each_head(dt):
 
 
 @pytest.mark.parametrize("dt,odt,d", [
-    (BF, BF, 64), (BF, BF, 128), (BF, F32, 64), (F32, F32, 64)])
+    (BF, BF, 64), (BF, BF, 128), (BF, F32, 64), (BF, F32, 128),
+    (F32, F32, 64), (F32, F32, 128)])
 @pytest.mark.parametrize("L,per_query", [(270, False), (270, True),
                                          (1100, False), (1100, True)])
 def test_many_heads(dt, odt, d, L, per_query):
