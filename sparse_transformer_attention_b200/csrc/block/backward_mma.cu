@@ -541,9 +541,9 @@ backward_rows_mma(Args a, int ntile) {
     if (lane < nrow) {
       const float* p = s_part + t_row + lane;
       pm = p[0];
-#pragma unroll
+#pragma unroll 1
       for (int u = 1; u < kShare; ++u) pm = fmaxf(pm, p[3 * u * ROWS]);
-#pragma unroll
+#pragma unroll 1
       for (int u = 0; u < kShare; ++u) {
         const float f = ex2(p[3 * u * ROWS] - pm);
         pl = fmaf(p[(3 * u + 1) * ROWS], f, pl);
@@ -769,7 +769,7 @@ backward_rows_mma(Args a, int ntile) {
   // dQ: the parts of a group's warps, one after the other
   __syncthreads();
   float* s_dq = reinterpret_cast<float*>(sC);
-#pragma unroll 1
+#pragma unroll
   for (int u = 0; u < kShare; ++u) {
     if (u == hf) {
 #pragma unroll
