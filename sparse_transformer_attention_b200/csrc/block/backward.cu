@@ -22,9 +22,9 @@
 // backward_mma.cu.
 //
 // Measured, bf16, the whole call: 2 x 12 heads, n = 8192, d = 64, W = 64,
-// k = 32: 699 us, of which rows 289, sort 110, listed 185, columns 118; 2
-// heads on one, n = 32768, d = 128, windows 64 to 256, k = 64: 869 us (386,
-// 105, 190, 162).  The listed rows alone, 256 (512) bytes per entry in the
+// k = 32: 686 us, of which rows 294, sort 115, listed 184, columns 117; 2
+// heads on one, n = 32768, d = 128, windows 64 to 256, k = 64: 880 us (394,
+// 100, 190, 174).  The listed rows alone, 256 (512) bytes per entry in the
 // row pass and again in the listed pass, are 1.6 (2.2) GB from L2 each.
 #include "backward.cuh"
 

@@ -106,11 +106,11 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t* hi,
 // still there.  Two warps share 16 rows: in the window each takes every
 // second block of keys, in the Top-k eight rows.
 //
-// Measured: 196608 rows of 64 + 32 keys, d = 64: 289 us, of which a CTA's 64
+// Measured: 196608 rows of 64 + 32 keys, d = 64: 294 us, of which a CTA's 64
 // rows spend 16% on the index rows, 10% and 16% on the window's two passes and
 // 56% on the Top-k (68 GB/s per SM, about half of what its L2 port carries);
 // without Top-k keys it is 150 us, each 16 more of them 70 us.  65536 rows of
-// 64 to 256 + 64 keys, d = 128: 386 us.  Three CTAs of 80 registers per SM
+// 64 to 256 + 64 keys, d = 128: 394 us.  Three CTAs of 80 registers per SM
 // instead of two of 128 were slower (352 us at d = 64).
 constexpr int kRowWarps = 8;
 
@@ -804,8 +804,8 @@ backward_rows_mma(Args a, int ntile) {
 // for all of them made each wait, at every chunk, for the one with the most
 // rows in it.  The listed part is added at the end.
 //
-// Measured: 196608 keys seen by 64 rows each, d = 64: 118 us; 32768 keys seen
-// by 2 x 160 rows, d = 128: 162 us.  Bound by latency and issue at four (two)
+// Measured: 196608 keys seen by 64 rows each, d = 64: 117 us; 32768 keys seen
+// by 2 x 160 rows, d = 128: 174 us.  Bound by latency and issue at four (two)
 // warps per scheduler; two warps per 16 keys, one for each gradient, doubled
 // the warps and computed S^T twice: 174 and 237 us.
 constexpr int kColWarps = 4;
