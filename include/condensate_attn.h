@@ -410,8 +410,9 @@ CA_API ca_status condensate_attn_norm_rope_backward(
  * scalar one when per-head k_h were given), idx, idx_count and C_max what it
  * wrote.  The probabilities are recomputed; neither O nor a log-sum-exp is
  * read.  dQ [B, Hq, nq, d] and dK, dV [B, Hkv, L, d] are written whole, in
- * dtype (keys that no row attends to get zeros).  Sums are fp32 in an order
- * fixed by the inputs: equal calls give equal bits.
+ * dtype (keys that no row attends to get zeros); overlapping an input, the
+ * workspace or each other they are refused.  Sums are fp32 in an order fixed
+ * by the inputs: equal calls give equal bits.
  *
  * Of a row's idx entries only the Top-k ones are read (slots 1 .. |C_i| - 1
  * - W_i).  One outside [1, i - W_i], or a count that does not fit the row's

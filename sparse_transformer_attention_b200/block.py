@@ -189,7 +189,8 @@ def condensate_attn_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor],
     copy; k and v may be None).  inv_freq [rot / 2] float32 (None: no
     rotation); positions [B, n] int32, else token t is at pos0 + t.  Q
     [B, Hq, n, d], K, V [B, Hkv, n, d] are written where given, e.g. rows of
-    a cache `Kc[:, :, p:p + n]`, else allocated.
+    a cache `Kc[:, :, p:p + n]`, else allocated; they must not overlap each
+    other or an input (an output may be its own input with equal strides).
 
     Returns (Q, K, V).
     """
@@ -234,7 +235,8 @@ def condensate_attn_norm_rope_backward(
     """Gradients of condensate_attn_norm_rope from dQ [B, Hq, n, d], dK, dV
     [B, Hkv, n, d] and its inputs q, k (needed only with a norm weight).  dq,
     dk, dv (token-major; e.g. the parts of one fused gradient) are written
-    where given.  weight_grads=False leaves the weights' gradients out.
+    where given and, like there, overlap nothing else.  weight_grads=False
+    leaves the weights' gradients out.
 
     Returns (dq, dk, dv, dq_weight, dk_weight), None where there is none.
     """
@@ -319,7 +321,8 @@ def condensate_attn_prefill_backward(
     """Gradients of condensate_attn_prefill with respect to Q, K and V, the
     sets held constant: Q [B, Hq, nq, d], K, V [B, Hkv, L, d], W, k, W_i and
     W_h as in the forward call, idx [B, Hq, nq, C_max] and idx_count
-    [B, Hq, nq] as it returned them, dO [B, Hq, nq, d] of O's type.  With a
+    [B, Hq, nq] as it returned them, dO [B, Hq, nq, d] of O's type.  dQ, dK
+    and dV, where given, must not overlap an input or each other.  With a
     workspace of the caller's (the size function's bytes) the device status
     can be read by condensate_attn_status.
 

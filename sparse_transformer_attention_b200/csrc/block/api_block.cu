@@ -69,6 +69,15 @@ ca_status from_cuda(cudaError_t e) {
   return e == cudaErrorNotSupported ? CA_ERR_UNSUPPORTED : CA_ERR_CUDA;
 }
 
+struct Bytes {
+  const void* p;
+  size_t n;
+};
+bool overlap(const Bytes& a, const Bytes& b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return a.p && b.p && (x < y ? y - x < a.n : x - y < b.n);
+}
+
 // Largest Top-k of the backward pass: the prefill's.
 constexpr int kMaxK = 128;
 
@@ -193,6 +202,17 @@ ca_status condensate_attn_prefill_backward(
       dtype, o_dtype, B, nq, L, Hq, Hkv, d, k);
   if (need == 0) return CA_ERR_UNSUPPORTED;
   if (workspace_bytes < need) return CA_ERR_WORKSPACE;
+  // what is written, then what is read: later passes read the inputs again
+  const size_t es = dtype == CA_BF16 ? 2 : 4, eo = o_dtype == CA_BF16 ? 2 : 4;
+  const size_t rows = (size_t)B * Hq * nq, keys = (size_t)B * Hkv * L;
+  const Bytes grids[] = {
+      {dQ, rows * d * es}, {dK, keys * d * es}, {dV, keys * d * es},
+      {workspace, need}, {Q, rows * d * es}, {K, keys * d * es},
+      {V, keys * d * es}, {dO, rows * d * eo}, {idx, rows * C_max * 4},
+      {idx_count, rows * 4}, {W_i, (size_t)B * nq * 4}, {W_h, (size_t)Hq * 4}};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 12; ++j)
+      if (overlap(grids[i], grids[j])) return CA_ERR_INVALID_ARG;
   ca::BackwardArgs a;
   a.Q = Q; a.K = K; a.V = V; a.dO = dO;
   a.do_bf16 = o_dtype == CA_BF16;

@@ -126,6 +126,28 @@ def test_prefill_backward_refusals(lib, over, code):
     assert _prefill_backward(lib, **over) == code
 
 
+@pytest.mark.parametrize("out", ["dQ", "dK", "dV", "ws"])
+@pytest.mark.parametrize("other", ["Q", "K", "V", "dO", "idx", "cnt", "W_i",
+                                   "W_h", "dQ", "dK", "dV", "ws"])
+def test_prefill_backward_refuses_overlap(lib, out, other):
+    """Results that begin in another grid's last 16 bytes, and the reverse."""
+    if out == other:
+        return
+    names = ("Q", "K", "V", "dO", "idx", "cnt", "W_i", "W_h", "dQ", "dK",
+             "dV", "ws")
+    at = {n: (i + 1) << 40 for i, n in enumerate(names)}
+    need = ca.condensate_attn_prefill_backward_workspace_size(
+        torch.bfloat16, torch.float32, 1, 1000, 1000, 8, 2, 128, 16)
+    rows, keys = 8 * 1000, 2 * 1000
+    size = dict(Q=rows * 256, K=keys * 256, V=keys * 256, dO=rows * 512,
+                idx=rows * 81 * 4, cnt=rows * 4, W_i=4000, W_h=32,
+                dQ=rows * 256, dK=keys * 256, dV=keys * 256, ws=need)
+    for a, b in ((out, other), (other, out)):
+        over = dict(at)
+        over[a] = at[b] + size[b] // 16 * 16 - 16
+        assert _prefill_backward(lib, ws_bytes=need, **over) == INV
+
+
 def test_workspace_sizes(lib):
     f = ca.condensate_attn_prefill_backward_workspace_size
     b = torch.bfloat16
